@@ -51,13 +51,19 @@ dma_status_t device_ok() {
   return cached[dev] == 1 ? DMA_OK : DMA_ERR_UNSUPPORTED;
 }
 
+dma_status_t check_heads(int Hq, int Hkv, int d) {
+  if (Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0) return DMA_ERR_INVALID_ARG;
+  if (!hkv_ok(Hkv) || (d != 64 && d != 128) || Hq / Hkv > 8) return DMA_ERR_UNSUPPORTED;
+  return DMA_OK;
+}
+
 namespace {
 
-// Shape checks shared by every entry point (Lk is the key axis).
+// Shape checks shared by the entry points on contiguous caches (Lk is the key axis).
 dma_status_t check_shape(int B, int Lk, int Hq, int Hkv, int d, int w) {
-  if (B < 1 || Lk < 1 || Hq < 1 || Hkv < 1 || d < 1 || w < 1) return DMA_ERR_INVALID_ARG;
-  if (Hq % Hkv != 0) return DMA_ERR_INVALID_ARG;
-  if (!hkv_ok(Hkv) || (d != 64 && d != 128) || Hq / Hkv > 8) return DMA_ERR_UNSUPPORTED;
+  if (B < 1 || Lk < 1 || w < 1) return DMA_ERR_INVALID_ARG;
+  const dma_status_t st = check_heads(Hq, Hkv, d);
+  if (st != DMA_OK) return st;
   if (Lk > kMaxLen) return DMA_ERR_UNSUPPORTED;
   if (Lk > w && w > kMaxKeep) return DMA_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * Lk * (Hq > Hkv ? Hq : Hkv) >= (1LL << 31)) return DMA_ERR_UNSUPPORTED;
@@ -597,6 +603,7 @@ dma_status_t dma_check(void* workspace, int clear, dma_stream_t stream) {
   if (word == kDevErrNone) return DMA_OK;
   if (word == kDevErrBadLength) return DMA_ERR_BAD_LENGTH;
   if (word == kDevErrBadPosition) return DMA_ERR_BAD_POSITION;
+  if (word == kDevErrBadPage) return DMA_ERR_BAD_PAGE;
   return DMA_ERR_TIMEOUT;
 }
 
@@ -616,6 +623,7 @@ const char* dma_status_string(dma_status_t status) {
     case DMA_ERR_TIMEOUT: return "DMA_ERR_TIMEOUT";
     case DMA_ERR_BAD_LENGTH: return "DMA_ERR_BAD_LENGTH";
     case DMA_ERR_BAD_POSITION: return "DMA_ERR_BAD_POSITION";
+    case DMA_ERR_BAD_PAGE: return "DMA_ERR_BAD_PAGE";
   }
   return "DMA_ERR_UNKNOWN";
 }

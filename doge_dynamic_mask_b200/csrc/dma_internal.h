@@ -27,7 +27,8 @@ constexpr long long kWaitLimitCycles = 2000000000LL;
 enum DeviceError : uint32_t {
   kDevErrNone = 0,
   kDevErrBadLength = 6,      // a lengths[b] outside [1, Lk]
-  kDevErrBadPosition = 7,    // a prologue token whose cache row is outside [0, Lmax)
+  kDevErrBadPosition = 7,    // a token whose cache row is outside the cache
+  kDevErrBadPage = 8,        // a page table entry that was needed lies outside the pool
   kDevErrTimeoutBase = 100,  // 100 + site: a bounded wait gave up
 };
 
@@ -84,6 +85,56 @@ struct DecodePlan {
   int n_split;
 };
 
+// A paged cache and what a decode query sees of it.
+struct PagedCache {
+  const float* dt_pages;          // [num_pages, Hkv, page_size]
+  const int32_t* table;           // [B, max_pages]
+  const int32_t* lengths;         // [B]
+  long long page_stride16;        // 16-byte units between pages of k_pages / v_pages
+  int B, max_pages, num_pages, page_size;
+  int page_shift;                 // log2(page_size), or -1
+  int Hkv, d, w, window, sinks;   // window 0: every key below the length is visible
+  uint32_t* err;
+};
+
+// Kept keys of the rows that see more than w keys: [B, Hkv, cap] each, the
+// first w entries written.  row is the key's K / V row in 16-byte units.
+struct PagedLists {
+  uint32_t* row;
+  float* bias;                    // dt of the key
+  int cap;
+};
+
+// Warps that share a paged decode's work, at most (its partials are sized for them).
+constexpr int kPagedMaxWorkers = 2368;
+// Blocks of the prologue's backward, at most (a row of dw partials each).
+constexpr int kPbMaxBlocks = 1024;
+
+// Arguments of the append to a paged cache and of the prologue's backward, as the entry points take them.
+struct AppendPaged {
+  const void *q, *k, *v;
+  long long q_stride, k_stride, v_stride;
+  const float *q_norm_w, *k_norm_w, *W_dt, *A;
+  const int32_t *cu_tokens, *positions, *page_table;
+  void *q_out, *k_out, *k_pages, *v_pages;
+  float* dt_pages;
+  long long page_stride;
+  float eps, theta;
+  int T, B, max_pages, num_pages, page_size, Hq, Hkv, d;
+};
+struct PrologueBackward {
+  const void *q, *k;
+  long long q_stride, k_stride;
+  const float *q_norm_w, *k_norm_w;
+  const int32_t* positions;
+  const void *dq_out, *dk_out;
+  void *dq, *dk;
+  long long dq_stride, dk_stride;
+  float *dq_norm_w, *dk_norm_w, *part;
+  float eps, theta;
+  int B, L, Hq, Hkv, d;
+};
+
 struct Geometry {
   int B, Lq, Lk, Hq, Hkv, d, w;
 };
@@ -125,10 +176,11 @@ cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t s
 
 // Entry-point helpers shared by the C ABI's translation units: record a CUDA
 // error for dma_last_cuda_error() and return DMA_ERR_CUDA; the sm_100 device
-// check; and the argument checks of dma_decode_step (everything it verifies
+// check; the head shapes every entry point supports; and the argument checks of dma_decode_step (everything it verifies
 // before it enqueues work, workspace size aside).
 dma_status_t cuda_fail(cudaError_t e);
 dma_status_t device_ok();
+dma_status_t check_heads(int Hq, int Hkv, int d);
 dma_status_t check_decode_args(const void* q, const void* k_cache, const void* v_cache, const float* W_dt,
                                const float* A, const int32_t* lengths, int B, int Lk, int Hq, int Hkv, int d,
                                int keep_window_size, float scale, const float* dt_in, const void* out,
@@ -155,6 +207,12 @@ cudaError_t launch_decode_update(const void* v_cache, const float* W, const floa
 cudaError_t launch_prologue(const void* q, const void* k, const void* v, const float* q_w, const float* k_w,
                             float eps, float theta, const int32_t* positions, int B, int L, int Lmax, int Hq, int Hkv,
                             int d, void* q_out, void* k_cache, void* v_cache, uint32_t* err, cudaStream_t s);
+// paged cache: append, selection of the rows longer than the kept window, attention (part: per-worker partials)
+cudaError_t launch_append_paged(const AppendPaged& p, uint32_t* err, cudaStream_t s);
+cudaError_t launch_select_paged(const PagedCache& c, const PagedLists& lists, cudaStream_t s);
+cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, const void* q, const void* k_pages,
+                              const void* v_pages, int Hq, float scale, float* part, void* out, cudaStream_t s);
+cudaError_t launch_prologue_backward(const PrologueBackward& p, cudaStream_t s);
 // CDMoE routing: router logits on the tensor cores (2K in {32, 64, 128, 256},
 // hidden a multiple of 64), then routing and experts (one CTA per token).
 cudaError_t launch_cdmoe_logits(const void* h, const void* W_router, int T, int hidden, int K, float* logits,

@@ -35,7 +35,7 @@
 // for bit.
 #include <cuda_runtime.h>
 
-#include "common.cuh"
+#include "rope.cuh"
 
 namespace dma {
 namespace {
@@ -49,16 +49,6 @@ constexpr int kPrologueMinBlocks = 2;             // CTAs per SM
 constexpr int kPrologueMaxTokens = 16;            // tokens per stage
 constexpr int kPrologueAngles = kPrologueMaxTokens * 64 / kPrologueCompute;   // angles per thread and stage, at most
 constexpr int kPrologueStageBytes = 32 * 1024;   // rows of one ring stage (whole tokens)
-
-__device__ __forceinline__ unsigned long long mul_f32x2(unsigned long long a, unsigned long long b) {
-  unsigned long long d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-// two bf16 channels (one 32-bit word, low channel first) as packed float32
-__device__ __forceinline__ unsigned long long widen_bf16x2(uint32_t w) {
-  return f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
 
 // Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned)
 // from global to shared memory, completing on `bar` (complete-tx).
@@ -91,12 +81,6 @@ __device__ __forceinline__ bool compute_barrier_or(bool flag) {
   return r != 0;
 }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
-// theta^(-2i/d) / (2 pi) for i < d/2: each angle in turns is pos times one of
-// these, formed once per call in double precision by the launcher
-struct RopeTurns {
-  double t[64];
-};
 
 // One ring stage holds the rows of `nts` consecutive tokens of the CTA's
 // chunk: [q rows of those tokens][k rows][v rows], each region one bulk copy
@@ -256,10 +240,8 @@ __global__ void __launch_bounds__(kPrologueThreads, kPrologueMinBlocks)
           if (!in_cache) raise_error(err, kDevErrBadPosition);
           crow_s[(i % kPrologueCrowSlots) * nts + j] = in_cache ? b * Lmax + pos : -1;
         }
-        const double u = static_cast<double>(pos) * turns.t[c];
-        const float r = static_cast<float>(u - rint(u));
         float sn, cs;
-        sincospif(2.0f * r, &sn, &cs);
+        rope_cos_sin(static_cast<double>(pos), turns.t[c], cs, sn);
         a[j * D + c] = cs;
         a[j * D + D / 2 + c] = sn;
       }
@@ -371,9 +353,7 @@ cudaError_t launch_prologue(const void* q, const void* k, const void* v, const f
   const long long tokens = static_cast<long long>(B) * L;
   if (tokens > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   if (d != 64 && d != 128) return cudaErrorInvalidValue;
-  RopeTurns turns{};
-  const double log_theta = log(static_cast<double>(theta));
-  for (int i = 0; i < d / 2; ++i) turns.t[i] = exp(-2.0 * i / d * log_theta) * 0.15915494309189535;   // / (2 pi)
+  const RopeTurns turns = make_rope_turns(theta, d);
   const long long tbytes = static_cast<long long>(Hq + 2 * Hkv) * d * 2;   // one token's rows
   // tokens per stage: about 32 KB of rows (at most 16 tokens), three stages
   long long nts = kPrologueStageBytes / tbytes;

@@ -9,6 +9,7 @@ library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -22,9 +23,11 @@ _lib = ctypes.CDLL(_LIB_PATH)
 
 DMA_OK = 0
 STATUS = {0: "DMA_OK", 1: "DMA_ERR_INVALID_ARG", 2: "DMA_ERR_UNSUPPORTED", 3: "DMA_ERR_WORKSPACE",
-          4: "DMA_ERR_CUDA", 5: "DMA_ERR_TIMEOUT", 6: "DMA_ERR_BAD_LENGTH", 7: "DMA_ERR_BAD_POSITION"}
+          4: "DMA_ERR_CUDA", 5: "DMA_ERR_TIMEOUT", 6: "DMA_ERR_BAD_LENGTH", 7: "DMA_ERR_BAD_POSITION",
+          8: "DMA_ERR_BAD_PAGE"}
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_i64 = ctypes.c_int64
 _lib.dma_workspace_size.restype = _sz
 _lib.dma_workspace_size.argtypes = [_i] * 7
 _lib.dma_dt_scores.restype = _i
@@ -54,6 +57,18 @@ _lib.dma_backward_workspace_size.restype = _sz
 _lib.dma_backward_workspace_size.argtypes = [_i] * 6
 _lib.dma_backward_prefill.restype = _i
 _lib.dma_backward_prefill.argtypes = [_vp] * 6 + [_i] * 6 + [_f] + [_vp] * 11 + [_sz, _vp]
+_lib.dma_append_paged.restype = _i
+_lib.dma_append_paged.argtypes = [_vp] * 3 + [_i64] * 3 + [_vp] * 2 + [_f] * 2 + [_vp] * 5 + [_i] * 5 + [_i64] + [
+    _i] * 3 + [_vp] * 6 + [_sz, _vp]
+_lib.dma_decode_paged_workspace_size.restype = _sz
+_lib.dma_decode_paged_workspace_size.argtypes = [_i] * 9
+_lib.dma_decode_paged.restype = _i
+_lib.dma_decode_paged.argtypes = [_vp] * 6 + [_i] * 4 + [_i64] + [_i] * 6 + [_f] + [_vp] * 2 + [_sz, _vp]
+_lib.dma_prologue_backward_workspace_size.restype = _sz
+_lib.dma_prologue_backward_workspace_size.argtypes = [_i] * 5
+_lib.dma_prologue_backward.restype = _i
+_lib.dma_prologue_backward.argtypes = [_vp] * 2 + [_i64] * 2 + [_vp] * 2 + [_f] * 2 + [_vp] * 3 + [_i] * 5 + [
+    _vp] * 2 + [_i64] * 2 + [_vp] * 3 + [_sz, _vp]
 _lib.dma_selftest_wait.restype = _i
 _lib.dma_selftest_wait.argtypes = [_vp, _vp]
 _lib.dma_check.restype = _i
@@ -274,6 +289,164 @@ def dma_decode_step_cached(q, k_cache, v_cache, W_dt, A, lengths, keep_window_si
     return out
 
 
+def _tensor(name, t, dtype, shape, device, strided=False):
+    """Data pointer of an argument after checking what the library cannot see: its type, shape and device and,
+    unless the caller passes the strides on, that it is dense."""
+    if t.dtype is not dtype or t.device != device or t.shape != shape:
+        raise ValueError(f"{name}: {dtype} {tuple(shape)} on {device} is wanted, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if not strided and not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _token_stride(name, t):
+    """Elements between tokens of [.., H, d] whose head rows are dense (a slice of a wider projection's output)."""
+    d, st = t.shape[-1], t.stride()
+    if (st[-1] != 1 or (t.shape[-2] > 1 and st[-2] != d)
+            or (len(st) == 4 and t.shape[0] > 1 and st[0] != st[1] * t.shape[1])):
+        raise ValueError(f"{name}: its heads must be dense and its tokens evenly spaced")
+    if len(st) == 4 and t.shape[1] == 1:
+        return st[0] if t.shape[0] > 1 else t.shape[-2] * d
+    return st[-3] if t.shape[-3] > 1 else t.shape[-2] * d
+
+
+def _page_stride(k_pages, v_pages):
+    """Elements between the pages of both pools (the rest of a page is dense)."""
+    _, page_size, Hkv, d = k_pages.shape
+    st = k_pages.stride()
+    if (k_pages.shape != v_pages.shape or st != v_pages.stride() or st[3] != 1 or (Hkv > 1 and st[2] != d)
+            or (page_size > 1 and st[1] != Hkv * d)):
+        raise ValueError("k_pages and v_pages must have one shape and stride, with dense pages")
+    return st[0] if k_pages.shape[0] > 1 else page_size * Hkv * d
+
+
+def _placed(call):
+    """Runs a binding with its first tensor's device current and, when a stream is given, on that stream: what it
+    allocates then belongs to the stream that uses it."""
+    @functools.wraps(call)
+    def placed(q, *args, stream=None, **kw):
+        if not q.is_cuda:
+            raise ValueError("tensors passed to libdma must be CUDA tensors")
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return placed(q, *args, **kw)
+        if q.device.index != torch.cuda.current_device():
+            with torch.cuda.device(q.device):
+                return call(q, *args, **kw)
+        return call(q, *args, **kw)
+    return placed
+
+
+@_placed
+def dma_append_paged(q, k, v, q_norm_w, k_norm_w, W_dt, A, cu_tokens, positions, page_table, k_pages, v_pages,
+                     dt_pages, eps=1e-6, rope_theta=10000.0, q_out=None, k_out=None, workspace=None):
+    """q/k RMSNorm and rotary embedding of a ragged batch's new tokens (packed [T, H, d]; sequence b owns tokens
+    cu_tokens[b] .. cu_tokens[b + 1] - 1, at positions from positions[b] on), K and V to their pages, dt to
+    dt_pages.  q, k and v may be slices of one projection's output.  Returns q_out; with k_out ([T, Hkv, d]) the
+    rotated K rows are written there too.  Takes `stream=` like every call here."""
+    T, Hq, d = q.shape
+    N, page_size, Hkv, _ = k_pages.shape
+    B, max_pages = page_table.shape
+    dev, bf, f32, i32 = q.device, torch.bfloat16, torch.float32, torch.int32
+    if q_out is None:
+        q_out = torch.empty((T, Hq, d), dtype=bf, device=dev)
+    if workspace is None:
+        workspace = new_workspace(256, dev)
+    page_stride = _page_stride(k_pages, v_pages)
+    _ok(_lib.dma_append_paged(
+        _tensor("q", q, bf, (T, Hq, d), dev, True), _tensor("k", k, bf, (T, Hkv, d), dev, True),
+        _tensor("v", v, bf, (T, Hkv, d), dev, True), _token_stride("q", q), _token_stride("k", k),
+        _token_stride("v", v), _tensor("q_norm_w", q_norm_w, f32, (d,), dev),
+        _tensor("k_norm_w", k_norm_w, f32, (d,), dev), eps, rope_theta,
+        _tensor("W_dt", W_dt, f32, (Hkv * d, Hkv), dev), _tensor("A", A, f32, (Hkv,), dev),
+        _tensor("cu_tokens", cu_tokens, i32, (B + 1,), dev), _tensor("positions", positions, i32, (B,), dev),
+        _tensor("page_table", page_table, i32, (B, max_pages), dev), T, B, max_pages, N, page_size, page_stride,
+        Hq, Hkv, d, _tensor("q_out", q_out, bf, (T, Hq, d), dev),
+        None if k_out is None else _tensor("k_out", k_out, bf, (T, Hkv, d), dev),
+        _tensor("k_pages", k_pages, bf, (N, page_size, Hkv, d), dev, True),
+        _tensor("v_pages", v_pages, bf, (N, page_size, Hkv, d), dev, True),
+        _tensor("dt_pages", dt_pages, f32, (N, Hkv, page_size), dev),
+        _tensor("workspace", workspace, torch.uint8, workspace.shape, dev), workspace.numel(),
+        torch.cuda.current_stream().cuda_stream), "dma_append_paged")
+    return q_out
+
+
+def dma_decode_paged_workspace_size(B, max_pages, page_size, Hq, Hkv, d, keep_window_size, window=0, sinks=0) -> int:
+    return int(_lib.dma_decode_paged_workspace_size(B, max_pages, page_size, Hq, Hkv, d, keep_window_size, window,
+                                                    sinks))
+
+
+@_placed
+def dma_decode_paged(q, k_pages, v_pages, dt_pages, page_table, lengths, keep_window_size, window=0, sinks=0,
+                     scale=None, out=None, workspace=None):
+    """One new query per sequence ([B, Hq, d]) over a paged cache: of the keys a sequence of lengths[b] tokens
+    sees (all, or the last `window` and the first `sinks`) the keep_window_size best by dt_pages, with dt as an
+    additive bias.  A length of 0 gives a zero row."""
+    B, Hq, d = q.shape
+    N, page_size, Hkv, _ = k_pages.shape
+    max_pages = page_table.shape[1]
+    dev, bf = q.device, torch.bfloat16
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        size = dma_decode_paged_workspace_size(B, max_pages, page_size, Hq, Hkv, d, keep_window_size, window, sinks)
+        if size == 0:
+            raise ValueError("unsupported paged decode geometry")
+        workspace = new_workspace(size, dev)
+    page_stride = _page_stride(k_pages, v_pages)
+    _ok(_lib.dma_decode_paged(
+        _tensor("q", q, bf, (B, Hq, d), dev), _tensor("k_pages", k_pages, bf, (N, page_size, Hkv, d), dev, True),
+        _tensor("v_pages", v_pages, bf, (N, page_size, Hkv, d), dev, True),
+        _tensor("dt_pages", dt_pages, torch.float32, (N, Hkv, page_size), dev),
+        _tensor("page_table", page_table, torch.int32, (B, max_pages), dev),
+        _tensor("lengths", lengths, torch.int32, (B,), dev), B, max_pages, N, page_size, page_stride, Hq, Hkv, d,
+        keep_window_size, window, sinks, d ** -0.5 if scale is None else scale,
+        _tensor("out", out, bf, (B, Hq, d), dev),
+        _tensor("workspace", workspace, torch.uint8, workspace.shape, dev), workspace.numel(),
+        torch.cuda.current_stream().cuda_stream), "dma_decode_paged")
+    return out
+
+
+def dma_prologue_backward_workspace_size(B, L, Hq, Hkv, d) -> int:
+    return int(_lib.dma_prologue_backward_workspace_size(B, L, Hq, Hkv, d))
+
+
+@_placed
+def dma_prologue_backward(q, k, q_norm_w, k_norm_w, positions, dq_out, dk_out, eps=1e-6, rope_theta=10000.0, dq=None,
+                          dk=None, dq_norm_w=None, dk_norm_w=None, workspace=None):
+    """Gradients of dma_prologue's norms and rotation from those of its rotated q and k ([B, L, H, d]): returns
+    (dq, dk) bf16 and (dq_norm_w, dk_norm_w) float32.  q, k, dq and dk may be slices of a projection's buffers."""
+    B, L, Hq, d = q.shape
+    Hkv = k.shape[2]
+    dev, bf, f32 = q.device, torch.bfloat16, torch.float32
+    if dq is None:
+        dq = torch.empty((B, L, Hq, d), dtype=bf, device=dev)
+    if dk is None:
+        dk = torch.empty((B, L, Hkv, d), dtype=bf, device=dev)
+    if dq_norm_w is None:
+        dq_norm_w = torch.empty(d, dtype=f32, device=dev)
+    if dk_norm_w is None:
+        dk_norm_w = torch.empty(d, dtype=f32, device=dev)
+    if workspace is None:
+        size = dma_prologue_backward_workspace_size(B, L, Hq, Hkv, d)
+        if size == 0:
+            raise ValueError("unsupported prologue geometry")
+        workspace = new_workspace(size, dev)
+    _ok(_lib.dma_prologue_backward(
+        _tensor("q", q, bf, (B, L, Hq, d), dev, True), _tensor("k", k, bf, (B, L, Hkv, d), dev, True),
+        _token_stride("q", q), _token_stride("k", k), _tensor("q_norm_w", q_norm_w, f32, (d,), dev),
+        _tensor("k_norm_w", k_norm_w, f32, (d,), dev), eps, rope_theta,
+        _tensor("positions", positions, torch.int32, (B,), dev), _tensor("dq_out", dq_out, bf, (B, L, Hq, d), dev),
+        _tensor("dk_out", dk_out, bf, (B, L, Hkv, d), dev), B, L, Hq, Hkv, d,
+        _tensor("dq", dq, bf, (B, L, Hq, d), dev, True), _tensor("dk", dk, bf, (B, L, Hkv, d), dev, True),
+        _token_stride("dq", dq), _token_stride("dk", dk), _tensor("dq_norm_w", dq_norm_w, f32, (d,), dev),
+        _tensor("dk_norm_w", dk_norm_w, f32, (d,), dev),
+        _tensor("workspace", workspace, torch.uint8, workspace.shape, dev), workspace.numel(),
+        torch.cuda.current_stream().cuda_stream), "dma_prologue_backward")
+    return dq, dk, dq_norm_w, dk_norm_w
+
+
 # keys per split of the decode attention: the kept lists are padded to a
 # multiple of it (the library's layout of a decode workspace)
 DECODE_CHUNK = 128
@@ -295,6 +468,19 @@ def decode_state_views(state, B, Lk, Hq, Hkv, d, keep_window_size):
     off = up(off + bg * cap * 4)             # bias
     count = state[off:off + bg * 4].view(torch.int32).view(B, Hkv)
     return dt, count, idx
+
+
+def paged_list_views(workspace, B, Hq, Hkv, d, keep_window_size):
+    """(row [B, Hkv, w] int64, bias [B, Hkv, w] float32) of a paged decode workspace with kept lists, for tests: a
+    key's row in 16-byte units of its pool (2^32 - 1: no key), and its dt.  Written for the rows that see more
+    than w keys."""
+    def up(x):
+        return -(-x // 256) * 256
+    n = B * Hkv * keep_window_size * 4
+    off = up(256 + 2368 * 2 * (Hq // Hkv) * (d + 2) * 4)
+    row = workspace[off:off + n].view(torch.int32).long() & 0xFFFFFFFF
+    bias = workspace[up(off + n):up(off + n) + n].view(torch.float32)
+    return row.view(B, Hkv, keep_window_size), bias.view(B, Hkv, keep_window_size)
 
 
 def dma_selftest_wait(workspace, stream=None):

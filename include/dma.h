@@ -67,7 +67,8 @@ typedef enum {
   DMA_ERR_CUDA = 4,        /* a CUDA call failed; dma_last_cuda_error() has the code */
   DMA_ERR_TIMEOUT = 5,     /* a bounded device wait gave up (reported by dma_check) */
   DMA_ERR_BAD_LENGTH = 6,  /* a lengths[b] outside [1, Lk] (reported by dma_check; clamped) */
-  DMA_ERR_BAD_POSITION = 7 /* a prologue token outside the cache (reported by dma_check; not written) */
+  DMA_ERR_BAD_POSITION = 7, /* a new token outside the cache (reported by dma_check; not written) */
+  DMA_ERR_BAD_PAGE = 8     /* a page table entry outside the pool (reported by dma_check; not touched) */
 } dma_status_t;
 
 /*
@@ -300,6 +301,107 @@ DMA_API dma_status_t dma_decode_step_cached(const void* q, const void* k_cache, 
                                             const float* W_dt, const float* A, const int32_t* lengths, int B,
                                             int Lk, int Hq, int Hkv, int d, int keep_window_size, float scale,
                                             void* out, void* state, size_t state_bytes, dma_stream_t stream);
+
+/*
+ * Backward of the prologue's norms and rotation ([DMA step 1]): from the
+ * gradients of its rotated outputs (dma_backward_prefill's dq and dk, when the
+ * prologue's q_out and appended K rows were that call's q and k) to those of
+ * its inputs.  V is appended unchanged, so its gradient needs no step.  For a
+ * head row x of token t of sequence b, with weight w, g the gradient of the
+ * rotated row and R the rotation by pos = positions[b] + t:
+ *   r = 1 / sqrt(mean(x^2) + eps),  dy = R^T g,
+ *   dx = r (w dy - x r^2 mean(x w dy)),  dw = sum over rows of dy x r
+ * in float32 (angles in double precision), dx rounded once to bf16.
+ *   q, k          [B, L, Hq, d], [B, L, Hkv, d] bf16: the prologue's inputs.  Token n = b * L + t
+ *                 of q starts q_stride elements after token n - 1 (k_stride for k): slices of
+ *                 one projection's output, or Hq * d (Hkv * d) for dense tensors
+ *   q_norm_w, k_norm_w, eps, rope_theta, positions  as in dma_prologue (positions may be any
+ *                 int32: nothing is addressed with them)
+ *   dq_out, dk_out  [B, L, Hq, d], [B, L, Hkv, d] bf16, dense
+ *   dq, dk        as q and k, with dq_stride and dk_stride (written)
+ *   dq_norm_w, dk_norm_w  [d] float32 (written, not added to)
+ *   workspace     dma_prologue_backward_workspace_size(...) bytes
+ * Strides are multiples of 8, at least heads * d.  Outputs must not overlap
+ * inputs.  The weight gradients' terms are added in a fixed order: the same call
+ * gives the same bits.  Supported: d in {64, 128}, Hkv in {1, 2, 4, 8, 16},
+ * Hq a multiple of Hkv, Hq / Hkv <= 8, B * L <= 2^30.
+ */
+DMA_API size_t dma_prologue_backward_workspace_size(int B, int L, int Hq, int Hkv, int d);
+DMA_API dma_status_t dma_prologue_backward(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
+                                           const float* q_norm_w, const float* k_norm_w, float eps, float rope_theta,
+                                           const int32_t* positions, const void* dq_out, const void* dk_out, int B,
+                                           int L, int Hq, int Hkv, int d, void* dq, void* dk, int64_t dq_stride,
+                                           int64_t dk_stride, float* dq_norm_w, float* dk_norm_w, void* workspace,
+                                           size_t ws_bytes, dma_stream_t stream);
+
+/*
+ * Paged cache.  The keys and values of all sequences share one pool of pages of
+ * page_size tokens; position j of sequence b is row j % page_size of page
+ * page_table[b, j / page_size].
+ *   k_pages, v_pages  [num_pages, page_size, Hkv, d] bf16; consecutive pages start
+ *                     page_stride elements apart in both (page_size * Hkv * d when dense;
+ *                     more for pages inside larger blocks), a multiple of 8
+ *   dt_pages          [num_pages, Hkv, page_size] float32, dense: dt of the cached tokens
+ *   page_table        [B, max_pages] int32.  Entries that hold no needed position are not
+ *                     read as pages and may be anything; a needed entry outside
+ *                     [0, num_pages) is reported as DMA_ERR_BAD_PAGE through dma_check
+ * A sequence has at most max_pages * page_size tokens (at most 2^20); page_size
+ * is any positive number (one that is a multiple of 4 lets the selection read dt
+ * 16 bytes at a time).  B <= 65536; K and V pools of up to 64 GiB each.
+ *
+ * dma_append_paged: [DMA steps 1-3] for the new tokens of a ragged batch, in one
+ * launch: the prologue's norms and rotation of q and k, K and V to their
+ * pages, and dt = exp(A * softplus(v_flat W_dt)), which never changes once the
+ * token is cached, to dt_pages.  Token t of the packed batch, cu_tokens[b] <= t <
+ * cu_tokens[b + 1], sits at position positions[b] + t - cu_tokens[b] of sequence b.
+ *   q, k, v       [T, Hq, d], [T, Hkv, d], [T, Hkv, d] bf16 projected states; consecutive
+ *                 tokens start q_stride, k_stride, v_stride elements apart (as in
+ *                 dma_prologue_backward)
+ *   q_norm_w, k_norm_w, eps, rope_theta  as in dma_prologue;  W_dt, A  as in dma_dt_scores
+ *   cu_tokens     [B + 1] int32, ascending: first token of each sequence (equal neighbours: a
+ *                 sequence without new tokens).  Tokens below cu_tokens[0] or from
+ *                 cu_tokens[B] on (padding of a captured batch) are ignored and their
+ *                 q_out and k_out rows stay as they are
+ *   positions     [B] int32: tokens each sequence has cached before
+ *   T             tokens in the packed tensors, at most 2^30
+ *   q_out         [T, Hq, d] bf16 (written)
+ *   k_out         [T, Hkv, d] bf16 or NULL: the normalised and rotated K rows too, packed
+ *                 (for dma_forward_prefill over a prompt)
+ *   workspace     >= 256 bytes, zeroed once (status word).  A token whose position lies outside
+ *                 [0, max_pages * page_size) is reported as DMA_ERR_BAD_POSITION; its cache rows
+ *                 are not written, its q_out and k_out rows are.  The same holds for a bad page.
+ * Two tokens must not share a cache row.  Outputs must not overlap inputs.
+ *
+ * dma_decode_paged: [DMA steps 3-4] for one new query per sequence, as
+ * dma_decode_step computes them, over the paged cache and its cached dt.  With
+ * len = lengths[b], the query sits at position len - 1 (already appended) and sees
+ *   window == 0:  positions [0, len);
+ *   window > 0:   positions [0, sinks) and [len - window, len) (a sliding window and first
+ *                 tokens that stay visible; pages in between may be gone).
+ * Of those it keeps the keep_window_size best by dt (ties: lower index), and
+ *   out[b, h, :] = sum_j p_j v_j,  p = softmax_fp32(scale * q_h . k_j + dt_j) over the kept keys.
+ *   q, out        [B, Hq, d] bf16 (out written)
+ *   lengths       [B] int32 in [0, max_pages * page_size]; 0 is an empty slot of a padded batch,
+ *                 whose out row is zero.  Others are clamped and reported as DMA_ERR_BAD_LENGTH
+ *   keep_window_size  any positive number; dt >= 0 as dma_append_paged writes it
+ *   workspace     dma_decode_paged_workspace_size(...) bytes, zeroed once (status word first)
+ * Keys in a page outside the pool are not seen (and reported).  Rows of a page past the
+ * sequence's length are never used and may hold anything.  The same call gives the same bits.
+ */
+DMA_API dma_status_t dma_append_paged(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                                      int64_t v_stride, const float* q_norm_w, const float* k_norm_w, float eps,
+                                      float rope_theta, const float* W_dt, const float* A, const int32_t* cu_tokens,
+                                      const int32_t* positions, const int32_t* page_table, int T, int B,
+                                      int max_pages, int num_pages, int page_size, int64_t page_stride, int Hq,
+                                      int Hkv, int d, void* q_out, void* k_out, void* k_pages, void* v_pages,
+                                      float* dt_pages, void* workspace, size_t ws_bytes, dma_stream_t stream);
+DMA_API size_t dma_decode_paged_workspace_size(int B, int max_pages, int page_size, int Hq, int Hkv, int d,
+                                               int keep_window_size, int window, int sinks);
+DMA_API dma_status_t dma_decode_paged(const void* q, const void* k_pages, const void* v_pages, const float* dt_pages,
+                                      const int32_t* page_table, const int32_t* lengths, int B, int max_pages,
+                                      int num_pages, int page_size, int64_t page_stride, int Hq, int Hkv, int d,
+                                      int keep_window_size, int window, int sinks, float scale, void* out,
+                                      void* workspace, size_t ws_bytes, dma_stream_t stream);
 
 /*
  * dma_decode_step without a caller-provided workspace (the pages have no

@@ -352,6 +352,85 @@ def prologue(q, k, v, q_norm_w, k_norm_w, eps, theta, positions, k_cache, v_cach
     return q_out, kc, vc
 
 
+def prologue_backward(q, k, q_norm_w, k_norm_w, eps, theta, positions, dq_out, dk_out):
+    """Gradients of the prologue's norms and rotation (float64).
+
+    q [B, L, H_q, d], k [B, L, H_kv, d]: the prologue's inputs; dq_out, dk_out:
+    gradients of a loss with respect to its rotated outputs.  Per head row x:
+    dy = the rotation's transpose applied to the gradient (the angle negated),
+    rho = sqrt(mean(x^2) + eps), dw = sum dy x / rho and
+    dx = w dy / rho - x sum(w dy x) / (d rho^3).
+    Returns dq, dk, dq_norm_w, dk_norm_w.
+    """
+    res = []
+    for x, w, g in ((q, q_norm_w, dq_out), (k, k_norm_w, dk_out)):
+        x = np.asarray(x, dtype=np.float64)
+        w = np.asarray(w, dtype=np.float64)
+        g = np.asarray(g, dtype=np.float64)
+        d = x.shape[-1]
+        dx, dw = np.empty_like(x), np.zeros(d)
+        for b in range(x.shape[0]):
+            dy = rope(g[b], -(int(positions[b]) + np.arange(x.shape[1])), theta)
+            rho = np.sqrt((x[b] * x[b]).mean(-1, keepdims=True) + eps)
+            dw += (dy * x[b] / rho).sum((0, 1))
+            u = w * dy
+            dx[b] = u / rho - x[b] * (u * x[b]).sum(-1, keepdims=True) / (d * rho ** 3)
+        res += [dx, dw]
+    return res[0], res[2], res[1], res[3]
+
+
+# --------------------------------------------------------------------------
+# Paged cache.  Position j of sequence b is row j % page_size of page
+# table[b, j // page_size] of the pools k_pages / v_pages [N, page_size, H_kv, d]
+# and dt_pages [N, H_kv, page_size].
+# --------------------------------------------------------------------------
+
+def append_paged(q, k, v, q_norm_w, k_norm_w, eps, theta, W, A, cu_tokens, positions, table, k_pages, v_pages,
+                 dt_pages):
+    """The prologue and the score of packed new tokens ([T, H, d]; sequence b
+    owns tokens cu_tokens[b] .. cu_tokens[b + 1] - 1), token by token.  Returns
+    (q_out, k_out, k_pages, v_pages, dt_pages) in float64; rows of tokens that
+    belong to no sequence are NaN in q_out and k_out."""
+    q, k, v = (np.asarray(x, dtype=np.float64) for x in (q, k, v))
+    kp, vp, dp = (np.array(x, dtype=np.float64) for x in (k_pages, v_pages, dt_pages))
+    page_size = kp.shape[1]
+    q_out, k_out = np.full_like(q, np.nan), np.full_like(k, np.nan)
+    for b in range(len(positions)):
+        for t in range(int(cu_tokens[b]), int(cu_tokens[b + 1])):
+            pos = int(positions[b]) + t - int(cu_tokens[b])
+            q_out[t] = rope(rms_norm(q[t:t + 1], q_norm_w, eps), np.array([pos]), theta)[0]
+            k_out[t] = rope(rms_norm(k[t:t + 1], k_norm_w, eps), np.array([pos]), theta)[0]
+            page, off = int(table[b][pos // page_size]), pos % page_size
+            kp[page, off], vp[page, off] = k_out[t], v[t]
+            dp[page, :, off] = dt_scores64(v[t][None, None], W, A)[0, :, 0]
+    return q_out, k_out, kp, vp, dp
+
+
+def visible_positions(length, window, sinks):
+    """Cached positions a decode query at length - 1 sees: all of them, or,
+    with a window, the first `sinks` and the last `window`."""
+    return [j for j in range(length) if window == 0 or j < sinks or j >= length - window]
+
+
+def decode_paged(q, k_pages, v_pages, dt_pages, table, lengths, w, window, sinks, scale):
+    """decode_step over a paged cache with cached dt (float32) and a window:
+    each sequence's visible rows are gathered in order and decoded alone.  A
+    sequence of length 0 gives zeros."""
+    B, Hq, d = q.shape
+    page_size = k_pages.shape[1]
+    out = np.zeros((B, Hq, d))
+    for b in range(B):
+        j = np.array(visible_positions(int(lengths[b]), window, sinks), dtype=np.int64)
+        if len(j) == 0:
+            continue
+        page, off = np.asarray(table[b])[j // page_size], j % page_size
+        dt = np.asarray(dt_pages)[page, :, off].T.astype(np.float32)          # [H_kv, n]
+        out[b] = decode_step(np.asarray(q[b:b + 1]), np.asarray(k_pages)[page, off][None],
+                             np.asarray(v_pages)[page, off][None], None, None, [len(j)], w, scale,
+                             dt=dt[None])[0]
+    return out
+
+
 # --------------------------------------------------------------------------
 # CDMoE routing   [Guide §CDMoE]  section "跨域 MoE（CDMoE）：在稠密 checkpoint 上“叠加”稀疏专家"
 #   router_gate maps the hidden state to num_keys * 2 logits; a top-k runs on
