@@ -11,17 +11,19 @@
 //
 // Design.  Memory-bound: every kept K and V row is read once, 4 Hq/Hkv flops
 // per 2 bytes.  All rows of all sequences and kv heads form one axis of 16-key
-// tiles, and the warps of the grid take equal contiguous ranges of it, so
-// ragged batches and single long sequences fill the SMs alike; a warp that
-// ends or begins inside a row leaves a float32 partial (o, m, l) that a second
-// kernel joins, in the order of the axis.  A warp works alone: its tiles travel
-// by cp.async through a ring of its own (keys that do not exist are filled with
-// zeros and masked), with table entries and dt fetched further ahead.  The
-// products run on mma.m16n8k16 with the keys (and, for P V, the channels) on
-// the M side and the group's query heads, at most eight, on the N side: no
-// row of a tile is padding, which tcgen05's 128 rows could not offer to one
-// query, and the tensor work stays far below the copy time.  P is split into
-// two bf16 terms, so its rounding (2^-17) does not show in the output.
+// tiles, and the blocks of the grid, and their warps, take equal contiguous
+// ranges of it, so ragged batches and single long sequences fill the SMs
+// alike.  A warp that begins or ends inside a row leaves a float32 piece (o, m,
+// l); a block joins its warps' pieces, and of the blocks that share a row the
+// last one to finish joins theirs, always in the order of the axis.  A warp
+// works alone: its tiles travel by cp.async through a ring of its own (keys
+// that do not exist are filled with zeros and masked), with positions, table
+// entries and dt fetched further ahead.  The products run on mma.m16n8k16 with
+// the keys (and, for P V, the channels) on the M side and the group's query
+// heads, at most eight, on the N side: no row of a tile is padding, which
+// tcgen05's 128 rows could not offer to one query, and the tensor work stays
+// far below the copy time.  P is split into two bf16 terms, so its rounding
+// (2^-17) does not show in the output.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -39,7 +41,7 @@ struct DpCfg {
   static constexpr int kStages = D == 128 ? 3 : 6;
   static constexpr int kRowBytes = D * 2;
   static constexpr int kTileBytes = kTileKeys * kRowBytes;         // K rows (V rows follow)
-  static constexpr int kStageBytes = 2 * kTileBytes + kTileKeys * 4;   // + the keys' biases
+  static constexpr int kStageBytes = 2 * kTileBytes + kTileKeys * 8;   // + the keys' masks (0 or -inf) and dt
   static constexpr int kSmemBytes = kDpWarps * kStages * kStageBytes;
 };
 
@@ -48,13 +50,18 @@ struct DpArgs {
   PagedLists lists;
   const uint16_t *q, *k, *v;
   uint16_t* out;
-  float* part;        // [workers][2][Hq / Hkv][d + 2]: o, m, l of the pieces at a range's ends
+  float* warp_part;   // [blocks][kDpWarps][2][Hq / Hkv][d + 2]: o, m, l of the pieces at a warp range's ends
+  float* block_part;  // [blocks][2][Hq / Hkv][d + 2]: the same for the blocks' ranges
+  uint32_t* tickets;  // [blocks], zero between calls: finished blocks of the row that begins in a block and leaves it
   float scale;
-  int Hq, workers;
+  int Hq;
 };
 
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -111,10 +118,51 @@ struct Cursor {
 };
 
 // One key of a tile on its way to the ring, per lane (lane & 15 is the key).
-struct KeyRef {
-  uint32_t row;      // offset of its K / V row in 16-byte units, or kNoRow
-  float bias;        // dt
+struct KeyPos {
+  int j, b, g;         // position in sequence b (-1: no key), kv head
+  const float* dt;     // where a listed key's dt lies, else null
 };
+struct KeyPage {
+  int page, off, g;    // table entry, row of the page (-1: no key)
+  const float* dt;
+};
+
+// What a warp leaves of a row that its range cuts: slot 0 a row that began
+// before the range, slot 1 one that begins in it and goes on.
+enum : int { kNone = 0, kEnds = 1, kThrough = 2, kOpen = 3 };
+struct RowCut {
+  long long t0;      // the row's first tile on the axis
+  int nt, b, g;
+};
+
+// Joins n pieces of a row for four channels of a head: piece(i) points at
+// piece i's o[d], m, l of that head; e is the first channel.
+template <int D, class F>
+__device__ __forceinline__ void join_pieces(int n, int e, F&& piece, float& M, float& den, float4& num) {
+  M = -INFINITY;
+  den = 0.0f;
+  num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* p = piece(i);
+    const float2 lo = __ldcg(reinterpret_cast<const float2*>(p + e)), hi = __ldcg(reinterpret_cast<const float2*>(p + e + 2));
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + D));
+    const float N = fmaxf(M, ml.x);
+    const float f = M == N ? 1.0f : fast_exp2(M - N), w = ml.x == N ? (N == -INFINITY ? 0.0f : 1.0f) : fast_exp2(ml.x - N);
+    M = N;
+    den = fmaf(den, f, w * ml.y);
+    num.x = fmaf(num.x, f, w * lo.x);
+    num.y = fmaf(num.y, f, w * lo.y);
+    num.z = fmaf(num.z, f, w * hi.x);
+    num.w = fmaf(num.w, f, w * hi.y);
+  }
+}
+
+__device__ __forceinline__ void write_out(uint16_t* out, float den, const float4& num) {
+  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+  *reinterpret_cast<uint2*>(out) =
+      make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
+}
 
 template <int D>
 __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __grid_constant__ DpArgs a) {
@@ -124,129 +172,138 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
   constexpr int RPI = 32 / CPR;         // rows per copy step of a warp
   constexpr int STG = Cfg::kStages;
   extern __shared__ __align__(128) unsigned char ring_all[];
-  __shared__ uint32_t s_scan[64];
-  __shared__ long long s_pref[kDpThreads + 1];
+  __shared__ long long s_pref[kDpThreads];     // tiles of the sequences up to and with this one
+  __shared__ uint32_t s_warp[kDpWarps];
+  __shared__ RowCut s_cut[kDpWarps][2];
+  __shared__ int s_kind[kDpWarps][2];
+  __shared__ int s_last[2];
   const PagedCache& c = a.c;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  // ---- this warp's range [x0, x1) of the axis
+  // ---- the axis: U tiles; G blocks take at least a tile per warp
+  auto scan_step = [&](int b0, long long before) {   // over sequences [b0, b0 + kDpThreads)
+    uint32_t x = b0 + tid < c.B ? static_cast<uint32_t>(seq_tiles(c, b0 + tid)) : 0u;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+      if (lane >= d) x += y;
+    }
+    __syncthreads();   // the last step's sums have been read
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    uint32_t all = 0;
+#pragma unroll
+    for (int w = 0; w < kDpWarps; ++w) {
+      if (w < warp) x += s_warp[w];
+      all += s_warp[w];
+    }
+    s_pref[tid] = before + x;
+    return before + all;
+  };
   long long total = 0;
-  for (int b0 = 0; b0 < c.B; b0 += kDpThreads) {
-    uint32_t n;
-    block_exclusive_scan(b0 + tid < c.B ? static_cast<uint32_t>(seq_tiles(c, b0 + tid)) : 0u, s_scan, &n);
-    total += n;
-  }
+  for (int b0 = 0; b0 < c.B; b0 += kDpThreads) total = scan_step(b0, total);
   const long long U = total * c.Hkv;
-  const long long W = min(static_cast<long long>(a.workers), U);
-  const long long wk = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
-  const long long x0 = wk < W ? U * wk / W : 0, x1 = wk < W ? U * (wk + 1) / W : 0;
+  const long long G = min(static_cast<long long>(gridDim.x), (U + kDpWarps - 1) / kDpWarps);
+  if (static_cast<long long>(blockIdx.x) >= G) return;
+  const long long xb0 = U * blockIdx.x / G, xb1 = U * (blockIdx.x + 1LL) / G;
+  const long long x0 = xb0 + (xb1 - xb0) * warp / kDpWarps, x1 = xb0 + (xb1 - xb0) * (warp + 1) / kDpWarps;
+  const int count = static_cast<int>(x1 - x0);
   Cursor cur{};
   {
-    const long long y = x0 / c.Hkv;   // tiles of sequences before this one, rounded into it
+    const long long y = x0 / c.Hkv;   // tiles of sequences before x0's, rounded into it
     long long before = 0;
     for (int b0 = 0; b0 < c.B; b0 += kDpThreads) {
-      uint32_t n;
-      const uint32_t ex =
-          block_exclusive_scan(b0 + tid < c.B ? static_cast<uint32_t>(seq_tiles(c, b0 + tid)) : 0u, s_scan, &n);
-      s_pref[tid] = before + ex;
-      if (tid == 0) s_pref[kDpThreads] = before + n;
+      const long long next = c.B > kDpThreads ? scan_step(b0, before) : total;
       __syncthreads();
-      if (y >= before && y < before + n) {
-        int lo = 0, hi = kDpThreads;   // s_pref[lo] <= y < s_pref[hi]
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (s_pref[mid] <= y)
-            lo = mid;
-          else
-            hi = mid;
-        }
-        cur.b = b0 + lo;
+      if (y >= before && y < next) {
+        int n = 0;   // sequences of this step that end at or before y
+#pragma unroll
+        for (int i = 0; i < kDpThreads; i += 32) n += __popc(__ballot_sync(0xFFFFFFFFu, s_pref[i + lane] <= y));
+        cur.b = b0 + n;
         cur.enter(c);
-        const long long rem = x0 - s_pref[lo] * c.Hkv;
+        const long long rem = x0 - (n > 0 ? s_pref[n - 1] : before) * c.Hkv;
         cur.g = static_cast<int>(rem / cur.nt);
         cur.t = static_cast<int>(rem % cur.nt);
       }
-      before += n;
-      __syncthreads();
+      before = next;
     }
   }
-  const int count = static_cast<int>(x1 - x0);
-  if (count == 0) return;
+  if (lane < 2) s_kind[warp][lane] = kNone;
+  if (tid < 2) s_last[tid] = 0;
+  const int nrep = a.Hq / c.Hkv;
+  const size_t psize = static_cast<size_t>(nrep) * (D + 2);
+  float* my_part = a.warp_part + (static_cast<size_t>(blockIdx.x) * kDpWarps + warp) * 2 * psize;
 
-  // ---- the ring: fetch (table entry or list entry) -> resolve (dt) -> issue (rows)
+  // ---- the ring: position -> table entry -> copies of rows and dt, a tile apart
   unsigned char* ring = ring_all + static_cast<size_t>(warp) * STG * Cfg::kStageBytes;
   const uint32_t ring_u = smem_u32(ring);
   const int kl = lane & 15;
-  Cursor fc = cur;       // the fetch side's cursor
+  Cursor fc = cur;       // the fetching side's cursor
   int fetched = 0;
-  // what fetch left for resolve: a page (and the key's row of it), or a list entry
-  int f_page = 0, f_off = 0, f_g = 0;
-  KeyRef f_ref{kNoRow, 0.0f};
-  bool f_direct = false;
-  auto fetch = [&]() {
-    f_direct = false;
-    f_ref = KeyRef{kNoRow, 0.0f};
+  auto position = [&]() {
+    KeyPos p{-1, fc.b, fc.g, nullptr};
     if (fetched < count) {
       const int i = fc.t * kTileKeys + kl;
       if (i < fc.keys) {
         if (fc.listed) {
           const size_t at = (static_cast<size_t>(fc.b) * c.Hkv + fc.g) * a.lists.cap + i;
-          f_ref = KeyRef{a.lists.row[at], a.lists.bias[at]};
+          p.j = a.lists.pos[at];
+          p.dt = a.lists.bias + at;
         } else {
-          f_direct = true;
-          const int slot = page_slot(c, key_position(c, fc.view, i), f_off);
-          f_page = __ldg(c.table + static_cast<size_t>(fc.b) * c.max_pages + slot);
-          f_g = fc.g;
+          p.j = key_position(c, fc.view, i);
         }
       }
       fc.next(c);
     }
     ++fetched;
+    return p;
   };
-  auto resolve = [&]() {
-    KeyRef r = f_ref;
-    if (f_direct) {
-      const int page = checked_page(c, f_page);
-      if (page >= 0) {
-        r.row = row_offset16(c, page, f_off, f_g);
-        r.bias = __ldg(c.dt_pages + dt_offset(c, page, f_off, f_g));
-      }
+  auto entry = [&](const KeyPos& p) {
+    KeyPage e{0, -1, p.g, p.dt};
+    if (p.j >= 0) {
+      const int slot = page_slot(c, p.j, e.off);
+      e.page = __ldg(c.table + static_cast<size_t>(p.b) * c.max_pages + slot);
     }
-    return r;
+    return e;
   };
   const int cr = lane / CPR, cc = lane % CPR;
-  auto issue = [&](const KeyRef& r, int slot) {
+  KeyPos npos = position();
+  KeyPage next = entry(npos);
+  npos = position();
+  auto issue = [&](int slot) {   // the tile whose entries came last; then the next one's
+    const KeyPage k = next;
+    next = entry(npos);
+    npos = position();
+    const int page = k.off >= 0 ? checked_page(c, k.page) : -1;
+    const uint32_t krow = page >= 0 ? row_offset16(c, page, k.off, k.g) : kNoRow;
+    const float* dt = page < 0 ? c.dt_pages : k.dt ? k.dt : c.dt_pages + dt_offset(c, page, k.off, k.g);
     const uint32_t st = ring_u + slot * Cfg::kStageBytes;
 #pragma unroll
     for (int i = 0; i < kTileKeys / RPI; ++i) {
       const int row = i * RPI + cr;
-      const uint32_t off = __shfl_sync(0xFFFFFFFFu, r.row, row);
+      const uint32_t off = __shfl_sync(0xFFFFFFFFu, krow, row);
       const bool there = off != kNoRow;
       const size_t e = there ? (static_cast<size_t>(off) + cc) * 8 : 0;
       const uint32_t dst = st + row * Cfg::kRowBytes + ((cc ^ (row & 7)) << 4);
       cp_async16_zfill(dst, a.k + e, there);
       cp_async16_zfill(dst + Cfg::kTileBytes, a.v + e, there);
     }
-    if (lane < kTileKeys)
+    if (lane < kTileKeys) {
       *reinterpret_cast<float*>(ring + slot * Cfg::kStageBytes + 2 * Cfg::kTileBytes + 4 * lane) =
-          r.row != kNoRow ? r.bias * kLog2e : -INFINITY;
+          krow != kNoRow ? 0.0f : -INFINITY;
+      cp_async4_zfill(st + 2 * Cfg::kTileBytes + 4 * kTileKeys + 4 * lane, dt, krow != kNoRow);
+    }
   };
-  fetch();
-  KeyRef ref = resolve();
-  fetch();
 #pragma unroll
   for (int s = 0; s < STG - 1; ++s) {
-    if (s < count) issue(ref, s);
+    if (s < count) issue(s);
     cp_commit();
-    ref = resolve();
-    fetch();
   }
 
   // ---- the tiles
   const int gid = lane >> 2, t4 = lane & 3;
-  const int nrep = a.Hq / c.Hkv;
   const float sl = a.scale * kLog2e;
   // ldmatrix addresses: K rows (row of the lane's 8x8 block, chunk parity), V rows transposed
   const int k_row = ((lane >> 3) & 1) * 8 + (lane & 7), k_par = lane >> 4;
@@ -275,10 +332,8 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
     __syncwarp();   // every lane's copies of this stage have landed; the previous stage has been read
     {
       const int nslot = slot == 0 ? STG - 1 : slot - 1;
-      if (x + STG - 1 < count) issue(ref, nslot);
+      if (x + STG - 1 < count) issue(nslot);
       cp_commit();
-      ref = resolve();
-      fetch();
     }
     const uint32_t st = ring_u + slot * Cfg::kStageBytes;
     float sa[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -291,7 +346,8 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
       mma16816(sb, kb, qf[s + 1][0], qf[s + 1][1]);
     }
     const float* bias = reinterpret_cast<const float*>(ring + slot * Cfg::kStageBytes + 2 * Cfg::kTileBytes);
-    const float b0 = bias[gid], b1 = bias[gid + 8];
+    const float b0 = fmaf(bias[kTileKeys + gid], kLog2e, bias[gid]),
+                b1 = fmaf(bias[kTileKeys + gid + 8], kLog2e, bias[gid + 8]);   // -inf where there is no key
     // scores in log2 units: keys gid and gid + 8, heads 2 t4 and 2 t4 + 1
     const float s00 = b0 == -INFINITY ? -INFINITY : fmaf(sa[0] + sb[0], sl, b0);
     const float s01 = b0 == -INFINITY ? -INFINITY : fmaf(sa[1] + sb[1], sl, b0);
@@ -363,8 +419,9 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
           }
         }
       } else {
-        // slot 1: the piece begins its row here and ends elsewhere; slot 0: the row began before
-        float* dst = a.part + ((wk * 2 + (from_start ? 1 : 0)) * nrep + ha) * (D + 2);
+        // slot 0: the row began before this range; slot 1: it begins here and goes on
+        const int cut = from_start ? 1 : 0;
+        float* dst = my_part + cut * psize + static_cast<size_t>(ha) * (D + 2);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           if (ha < nrep) {
@@ -384,82 +441,115 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
           dst[2 * D + 2] = m1;
           dst[2 * D + 3] = L1;
         }
+        if (lane == 0) {
+          s_kind[warp][cut] = cut ? kOpen : (row_end ? kEnds : kThrough);
+          s_cut[warp][cut] = RowCut{x0 + x - cur.t, cur.nt, cur.b, cur.g};
+        }
       }
       fresh = true;
     }
     cur.next(c);
   }
   cp_wait<0>();
-}
+  __syncthreads();   // every warp's pieces are written
 
-// Joins the pieces of rows that more than one warp worked on, in the order of
-// the axis: one block per (sequence, query head), a thread per channel.
-template <int D>
-__global__ void __launch_bounds__(D) decode_paged_join_kernel(const __grid_constant__ DpArgs a) {
-  __shared__ long long s_sum[2];
-  const PagedCache& c = a.c;
-  pdl_wait();
-  const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
-  const int nrep = a.Hq / c.Hkv, g = h / nrep;
-  if (threadIdx.x < 2) s_sum[threadIdx.x] = 0;
+  // ---- the block's pieces, row by row.  Chain w < kDpWarps: the row that begins
+  // in warp w and leaves its range; chain kDpWarps: the row that began before the
+  // block.  The warps share out (chain, 128 channels of its heads).
+  const float* warp_part = a.warp_part + static_cast<size_t>(blockIdx.x) * kDpWarps * 2 * psize;
+  float* my_block = a.block_part + static_cast<size_t>(blockIdx.x) * 2 * psize;
+  const int parts = (nrep * D + 127) / 128;
+  int first = 0;   // the block's first warp with tiles
+  while (xb0 + (xb1 - xb0) * (first + 1) / kDpWarps == xb0) ++first;
+  const bool left = s_kind[first][0] != kNone;
+  int shared = 0, open = -1;   // items so far; the chain that goes on past the block
+  for (int w = 0; w <= kDpWarps; ++w) {
+    if (w < kDpWarps ? s_kind[w][1] != kOpen : !left) continue;
+    const int w0 = w < kDpWarps ? w : first;
+    const RowCut cut = s_cut[w0][w < kDpWarps ? 1 : 0];
+    const long long end = min(cut.t0 + cut.nt, xb1);
+    const int w1 = static_cast<int>(((end - xb0) * kDpWarps - 1) / (xb1 - xb0));   // the warp of its last tile here
+    const bool right = cut.t0 + cut.nt > xb1;
+    if (right) open = w;
+    for (int q = 0; q < parts; ++q, ++shared) {
+      if (shared % kDpWarps != warp) continue;
+      const int e = q * 128 + 4 * lane, h = e / D;
+      if (h >= nrep) continue;
+      int n = 0;
+      uint32_t order = 0;   // the chain's warps that have tiles, four bits each
+      for (int i = w0; i <= w1; ++i)
+        if (s_kind[i][0] != kNone || i == w0) order |= static_cast<uint32_t>(i) << (4 * n++);
+      const float* base = warp_part + static_cast<size_t>(h) * (D + 2);
+      float M, den;
+      float4 num;
+      join_pieces<D>(
+          n, e % D,
+          [&](int i) { return base + (2 * (order >> (4 * i) & 15u) + (i == 0 && w < kDpWarps ? 1 : 0)) * psize; }, M, den,
+          num);
+      if (w < kDpWarps && !right) {
+        write_out(a.out + (static_cast<size_t>(cut.b) * a.Hq + cut.g * nrep + h) * D + e % D, den, num);
+      } else {
+        float* dst = my_block + (w < kDpWarps ? psize : 0) + static_cast<size_t>(h) * (D + 2);
+        *reinterpret_cast<float2*>(dst + e % D) = make_float2(num.x, num.y);
+        *reinterpret_cast<float2*>(dst + e % D + 2) = make_float2(num.z, num.w);
+        if (e % D == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(M, den);
+      }
+    }
+  }
+
+  // ---- rows shared with other blocks: the one that finishes such a row's last
+  // piece joins them
+  const bool two = open >= 0 && open < kDpWarps;   // a row that goes on and began here (else it is the left one)
+  if (!left && !two) return;
+  auto row_blocks = [&](int k, long long& b0, long long& b1) {
+    const RowCut r = k == 0 ? s_cut[first][0] : s_cut[open][1];
+    b0 = (G * (r.t0 + 1) - 1) / U;
+    b1 = (G * (r.t0 + r.nt) - 1) / U;
+    return r;
+  };
   __syncthreads();
-  long long before = 0, all = 0;
-  for (int i = threadIdx.x; i < c.B; i += D) {
-    const int n = seq_tiles(c, i);
-    all += n;
-    before += i < b ? n : 0;
-  }
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) {
-    all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
-    before += __shfl_xor_sync(0xFFFFFFFFu, before, d);
-  }
-  if ((threadIdx.x & 31) == 0) {
-    atomicAdd(reinterpret_cast<unsigned long long*>(&s_sum[0]), static_cast<unsigned long long>(all));
-    atomicAdd(reinterpret_cast<unsigned long long*>(&s_sum[1]), static_cast<unsigned long long>(before));
+  if (lane == 0 && warp < 2 && (warp == 0 ? left : two)) {
+    long long b0, b1;
+    row_blocks(warp, b0, b1);
+    __threadfence();
+    if (atomicAdd(a.tickets + b0, 1u) == static_cast<uint32_t>(b1 - b0)) {
+      a.tickets[b0] = 0u;
+      s_last[warp] = 1;
+    }
+    __threadfence();
   }
   __syncthreads();
-  const long long U = s_sum[0] * c.Hkv, W = min(static_cast<long long>(a.workers), U);
-  const int nt = seq_tiles(c, b);
-  const long long t0 = s_sum[1] * c.Hkv + static_cast<long long>(g) * nt, t1 = t0 + nt;   // the row on the axis
-  const long long w0 = (W * (t0 + 1) - 1) / U, w1 = (W * t1 - 1) / U;                     // its first and last warp
-  if (w0 == w1) return;   // one warp had it all and has written it
-  const int e = threadIdx.x;
-  const size_t slot = static_cast<size_t>(nrep) * (D + 2);
-  const float* p0 = a.part + w0 * 2 * slot + static_cast<size_t>(h - g * nrep) * (D + 2);
-  const int np = static_cast<int>(w1 - w0) + 1;
-  // the first warp's piece is in slot 1 when the row begins inside or at the start of its range
-  auto piece = [&](int i) { return p0 + (i == 0 ? 1 : 2 * i) * slot; };
-  float M = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < np; ++i) M = fmaxf(M, piece(i)[D]);
-  float num = 0.0f, den = 0.0f;
-#pragma unroll 8
-  for (int i = 0; i < np; ++i) {
-    const float* p = piece(i);
-    const float wgt = p[D] == -INFINITY ? 0.0f : fast_exp2(p[D] - M);
-    num = fmaf(wgt, p[e], num);
-    den = fmaf(wgt, p[D + 1], den);
+  for (int k = 0; k < 2; ++k) {
+    if (!s_last[k]) continue;
+    long long b0, b1;
+    const RowCut r = row_blocks(k, b0, b1);
+    for (int q = warp; q < parts; q += kDpWarps) {
+      const int e = q * 128 + 4 * lane, h = e / D;
+      if (h >= nrep) continue;
+      const float* base = a.block_part + static_cast<size_t>(b0) * 2 * psize + static_cast<size_t>(h) * (D + 2);
+      float M, den;
+      float4 num;
+      join_pieces<D>(
+          static_cast<int>(b1 - b0) + 1, e % D, [&](int i) { return base + (i == 0 ? 1 : 2 * i) * psize; }, M, den, num);
+      write_out(a.out + (static_cast<size_t>(r.b) * a.Hq + r.g * nrep + h) * D + e % D, den, num);
+    }
   }
-  reinterpret_cast<__nv_bfloat16*>(a.out)[static_cast<size_t>(blockIdx.x) * D + e] =
-      __float2bfloat16_rn(den == 0.0f ? 0.0f : num / den);
 }
 
 template <int D>
 cudaError_t launch_dp(const DpArgs& a, int blocks, cudaStream_t s) {
-  cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(decode_paged_kernel<D>), DpCfg<D>::kSmemBytes);
+  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(decode_paged_kernel<D>), DpCfg<D>::kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_after(decode_paged_kernel<D>, dim3(blocks), dim3(kDpThreads), DpCfg<D>::kSmemBytes, s, a);
-  if (e != cudaSuccess) return e;
-  return launch_after(decode_paged_join_kernel<D>, dim3(static_cast<unsigned>(a.c.B) * a.Hq), dim3(D), 0, s, a);
+  return launch_after(decode_paged_kernel<D>, dim3(blocks), dim3(kDpThreads), DpCfg<D>::kSmemBytes, s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, const void* q, const void* k_pages,
-                              const void* v_pages, int Hq, float scale, float* part, void* out, cudaStream_t s) {
+                              const void* v_pages, int Hq, float scale, void* scratch, void* out, cudaStream_t s) {
   const int nsm = sm_count();
   if (nsm <= 0) return cudaErrorInvalidDevice;
+  const size_t psize = static_cast<size_t>(Hq / c.Hkv) * (c.d + 2);
   DpArgs a;
   a.c = c;
   a.lists = lists;
@@ -467,12 +557,18 @@ cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, cons
   a.k = static_cast<const uint16_t*>(k_pages);
   a.v = static_cast<const uint16_t*>(v_pages);
   a.out = static_cast<uint16_t*>(out);
-  a.part = part;
+  a.tickets = static_cast<uint32_t*>(scratch);
+  a.block_part = reinterpret_cast<float*>(static_cast<char*>(scratch) + kPagedMaxBlocks * 4);
+  a.warp_part = a.block_part + kPagedMaxBlocks * 2 * psize;
   a.scale = scale;
   a.Hq = Hq;
-  const int blocks = std::min(nsm, kPagedMaxWorkers / kDpWarps);
-  a.workers = blocks * kDpWarps;
+  const int blocks = std::min(nsm, kPagedMaxBlocks);
   return c.d == 64 ? launch_dp<64>(a, blocks, s) : launch_dp<128>(a, blocks, s);
+}
+
+size_t attn_paged_scratch_bytes(int Hq, int Hkv, int d) {
+  return kPagedMaxBlocks * 4 +
+         static_cast<size_t>(kPagedMaxBlocks) * (1 + kDpWarps) * 2 * (Hq / Hkv) * (d + 2) * sizeof(float);
 }
 
 }  // namespace dma

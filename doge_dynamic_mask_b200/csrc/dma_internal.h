@@ -98,15 +98,15 @@ struct PagedCache {
 };
 
 // Kept keys of the rows that see more than w keys: [B, Hkv, cap] each, the
-// first w entries written.  row is the key's K / V row in 16-byte units.
+// first w entries written.
 struct PagedLists {
-  uint32_t* row;
-  float* bias;                    // dt of the key
+  int32_t* pos;                   // position in the sequence (-1: no key)
+  float* bias;                    // its dt
   int cap;
 };
 
-// Warps that share a paged decode's work, at most (its partials are sized for them).
-constexpr int kPagedMaxWorkers = 2368;
+// Blocks that share a paged decode's work, at most (its scratch is sized for them).
+constexpr int kPagedMaxBlocks = 256;
 // Blocks of the prologue's backward, at most (a row of dw partials each).
 constexpr int kPbMaxBlocks = 1024;
 
@@ -207,11 +207,13 @@ cudaError_t launch_decode_update(const void* v_cache, const float* W, const floa
 cudaError_t launch_prologue(const void* q, const void* k, const void* v, const float* q_w, const float* k_w,
                             float eps, float theta, const int32_t* positions, int B, int L, int Lmax, int Hq, int Hkv,
                             int d, void* q_out, void* k_cache, void* v_cache, uint32_t* err, cudaStream_t s);
-// paged cache: append, selection of the rows longer than the kept window, attention (part: per-worker partials)
+// paged cache: append, selection of the rows longer than the kept window, attention
+// (scratch: attn_paged_scratch_bytes, zeroed before its first use)
 cudaError_t launch_append_paged(const AppendPaged& p, uint32_t* err, cudaStream_t s);
 cudaError_t launch_select_paged(const PagedCache& c, const PagedLists& lists, cudaStream_t s);
 cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, const void* q, const void* k_pages,
-                              const void* v_pages, int Hq, float scale, float* part, void* out, cudaStream_t s);
+                              const void* v_pages, int Hq, float scale, void* scratch, void* out, cudaStream_t s);
+size_t attn_paged_scratch_bytes(int Hq, int Hkv, int d);
 cudaError_t launch_prologue_backward(const PrologueBackward& p, cudaStream_t s);
 // CDMoE routing: router logits on the tensor cores (2K in {32, 64, 128, 256},
 // hidden a multiple of 64), then routing and experts (one CTA per token).

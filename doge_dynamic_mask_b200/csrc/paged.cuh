@@ -53,11 +53,14 @@ __device__ __forceinline__ uint32_t row_offset16(const PagedCache& c, int page, 
          static_cast<uint32_t>((off * c.Hkv + g) * (c.d / 8));
 }
 
-__device__ __forceinline__ size_t dt_offset(const PagedCache& c, int page, int off, int g) {
-  return (static_cast<size_t>(page) * c.Hkv + g) * c.page_size + off;
+// Offset of a key's dt (32 bits hold it: a pool of K rows has at most 2^32
+// 16-byte units, so fewer than 2^30 rows of a head).
+__device__ __forceinline__ uint32_t dt_offset(const PagedCache& c, int page, int off, int g) {
+  return static_cast<uint32_t>(page) * static_cast<uint32_t>(c.Hkv * c.page_size) +
+         static_cast<uint32_t>(g * c.page_size + off);
 }
 
-// list entries and rows that stand for no key
+// a row offset that stands for no key
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
 }  // namespace dma

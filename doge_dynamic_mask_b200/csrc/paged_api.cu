@@ -38,22 +38,22 @@ long long visible_cap(int max_pages, int page_size, int window, int sinks) {
   return window > 0 ? std::min(cap, static_cast<long long>(window) + sinks) : cap;
 }
 
-// Paged decode workspace: header, partials, and, when a query may see more than
-// keep_window_size keys, the kept lists.
+// Paged decode workspace: header, the attention's scratch, and, when a query
+// may see more than keep_window_size keys, the kept lists.
 struct PagedWorkspace {
-  size_t part, row, bias, bytes;
+  size_t scratch, pos, bias, bytes;
   int cap;
 };
 
 PagedWorkspace paged_workspace(int B, int max_pages, int page_size, int Hq, int Hkv, int d, int w, int window, int sinks) {
   PagedWorkspace p{};
-  p.part = kHeaderBytes;
-  p.bytes = align_up(p.part + static_cast<size_t>(kPagedMaxWorkers) * 2 * (Hq / Hkv) * (d + 2) * 4, 256);
+  p.scratch = kHeaderBytes;
+  p.bytes = align_up(p.scratch + attn_paged_scratch_bytes(Hq, Hkv, d), 256);
   if (visible_cap(max_pages, page_size, window, sinks) > w) {
     p.cap = w;
     const size_t list = static_cast<size_t>(B) * Hkv * w * 4;
-    p.row = p.bytes;
-    p.bias = align_up(p.row + list, 256);
+    p.pos = p.bytes;
+    p.bias = align_up(p.pos + list, 256);
     p.bytes = align_up(p.bias + list, 256);
   }
   return p;
@@ -142,10 +142,10 @@ dma_status_t dma_decode_paged(const void* q, const void* k_pages, const void* v_
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (wsl.cap > 0) {
-    lists = PagedLists{reinterpret_cast<uint32_t*>(ws + wsl.row), reinterpret_cast<float*>(ws + wsl.bias), wsl.cap};
+    lists = PagedLists{reinterpret_cast<int32_t*>(ws + wsl.pos), reinterpret_cast<float*>(ws + wsl.bias), wsl.cap};
     if ((e = launch_select_paged(c, lists, s)) != cudaSuccess) return cuda_fail(e);
   }
-  e = launch_attn_paged(c, lists, q, k_pages, v_pages, Hq, scale, reinterpret_cast<float*>(ws + wsl.part), out, s);
+  e = launch_attn_paged(c, lists, q, k_pages, v_pages, Hq, scale, ws + wsl.scratch, out, s);
   return e == cudaSuccess ? DMA_OK : cuda_fail(e);
 }
 

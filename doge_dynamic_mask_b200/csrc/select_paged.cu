@@ -6,19 +6,22 @@
 // dt; ties go to the lower index).  dt of every cached token lies in its page.
 //
 // Design.  One cluster of CTAs per (sequence, kv head).  The row is read once:
-// a sample of 4096 keys (1024 quads spread over the row) gives a threshold that
-// the w-th best key is above with four standard deviations to spare, every
-// warp collects the keys at or above it from 128-key chunks dealt out in turn,
-// and the collected keys (about 1.4 w at 64k keys) are cut to the w best: a
-// histogram over the cluster finds the bin of the w-th, keys above the bin are
-// kept, and the few keys inside are ranked one against another by (dt, index).
-// The bound is the one read of dt plus the latency of those steps; a row is
-// spread over up to eight CTAs when there are fewer rows than SMs.  Rows the
-// sample misjudges (more ties at the threshold than the buffers hold, too few
-// keys) are selected exactly by the cluster's first CTA in a few more passes.
-// The order of the list is fixed by the row alone (chunk dealing, then rank),
-// so the attention adds its terms in the same order every time.
+// a sample (2048 keys, of long rows 4096, in runs of eight spread over the row)
+// gives a threshold that the w-th best key is above with four standard
+// deviations to spare, and every warp appends the keys at or above it that it
+// meets (about 1.6 w in all at 64k keys) to a list of its own in shared memory.
+// A histogram of the collected keys over the cluster finds the w-th key's bin;
+// keys above the bin are kept, and the few inside are ranked one against
+// another by (dt, index).  The bound is the one read of dt plus the latency of
+// those steps; a row is spread over up to eight CTAs when there are fewer rows
+// than SMs.  Rows the sample misjudges (more ties at the threshold than the
+// lists hold, too few keys) are selected exactly by the cluster's first CTA in a
+// few more passes.  The order of the list is fixed by the row alone, so the
+// attention adds its terms in the same order every time.
 #include <cooperative_groups.h>
+
+#include <algorithm>
+#include <cmath>
 
 #include "paged.cuh"
 #include "select_common.cuh"
@@ -28,102 +31,119 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSpThreads = 256;
-constexpr int kSpWarps = kSpThreads / 32;
-constexpr int kSpMinBlocks = 3;
-constexpr int kSpRegion = 768;           // collected keys per warp
-constexpr int kSpSampleQuads = 1024;
-constexpr int kSpEdge = 1024;            // keys inside the w-th key's bin
-constexpr int kSpChunks = 4;             // 128-key chunks in flight per warp
-
-struct SpSmem {
-  uint64_t keys[kSpWarps][kSpRegion];    // collected keys; first the sample
-  uint64_t edge[kSpEdge];                // (first CTA) keys inside the w-th key's bin
-  uint32_t hist[kBins];
-  uint64_t vars[8];
-  uint32_t red[64];
-  uint32_t count[kSpWarps];              // collected per warp, then kept per warp
-  uint32_t stat[8];                      // cluster exchange, see the uses
+constexpr int kSpSample = 512;           // sampled octs (runs of eight positions), at most
+constexpr int kSpSampleLong = 131072;    // rows up to this length take half of them
+constexpr int kSpEdge = 512;             // keys inside the w-th key's bin
+// many rows: 256 threads, four CTAs per SM; rows split over a cluster: 1024
+// threads, one CTA per SM
+template <int THREADS>
+struct SpCfg {
+  static constexpr int kMinBlocks = THREADS == 256 ? 4 : 1;
+  static constexpr int kSample = kSpSample > THREADS ? kSpSample / THREADS : 1;   // sampled octs per thread
+  static constexpr int kUnroll = 2;                                               // octs in flight per thread
 };
 
-// A row's visible keys as quads of four positions (16 bytes of dt when the
-// page size is a multiple of four): quads [0, nqa) cover the sinks, the rest the
-// positions from `start` on.
+struct SpShared {
+  __align__(16) uint32_t hist[kBins];
+  uint64_t edge[kSpEdge];                // (first CTA) keys inside the w-th key's bin
+  uint32_t warp[3][32];                  // per-warp values
+  uint32_t bin[3];                       // top_bin's answer
+  uint32_t keys, sure, overflow;         // this CTA's collected keys, those above the bin, lists that ran over
+  uint32_t edges, exact;                 // (first CTA) keys in `edge`; the row needs the exact selection
+};
+// dynamic shared memory: SpShared, then [warps][room] collected keys (the
+// sample's values before them)
+
+// A row's visible keys as octs of eight positions: octs [0, noa) cover the
+// sinks, the rest the positions from `start` on.
 struct Row {
-  int b, g, sinks, start, len, nqa, nq, qb;
+  const int32_t* table;
+  int g, sinks, start, len, noa, no, ob;
 };
 
 __device__ __forceinline__ Row make_row(const PagedCache& c, const SeqView& v, int b, int g) {
   Row r;
-  r.b = b;
+  r.table = c.table + static_cast<size_t>(b) * c.max_pages;
   r.g = g;
   r.len = v.len;
   r.sinks = v.shift > 0 ? c.sinks : 0;
   r.start = v.shift > 0 ? c.sinks + v.shift : 0;
-  r.nqa = (r.sinks + 3) >> 2;
-  r.qb = r.start >> 2;
-  r.nq = r.nqa + ((r.len + 3) >> 2) - r.qb;
+  r.noa = (r.sinks + 7) >> 3;
+  r.ob = r.start >> 3;
+  r.no = r.noa + ((r.len + 7) >> 3) - r.ob;
   return r;
 }
 
-__device__ __forceinline__ int quad_position(const Row& r, int x) { return 4 * (x < r.nqa ? x : x - r.nqa + r.qb); }
+__device__ __forceinline__ int oct_position(const Row& r, int x) { return 8 * (x < r.noa ? x : x - r.noa + r.ob); }
 
-__device__ __forceinline__ bool quad_sees(const Row& r, int x, int j) {
-  return x < r.nqa ? j < r.sinks : (j >= r.start && j < r.len);
+// which of an oct's positions from j0 on are visible (bit e)
+__device__ __forceinline__ uint32_t oct_mask(const Row& r, int x, int j0) {
+  if (x > r.noa && x + 1 < r.no) return 255u;   // inside the second range
+  const int lo = x < r.noa ? 0 : r.start, hi = x < r.noa ? r.sinks : r.len;
+  const uint32_t below = (1u << min(8, max(0, lo - j0))) - 1u;
+  return ((1u << min(8, max(0, hi - j0))) - 1u) & ~below;
 }
 
-// The quad's table entry (page size a multiple of four): x in [0, nq).
-__device__ __forceinline__ int quad_page(const PagedCache& c, const Row& r, int x) {
+// The table entry of an oct's first position (0 past the row).
+__device__ __forceinline__ int oct_page(const PagedCache& c, const Row& r, int x) {
+  if (x >= r.no) return 0;
   int off;
-  const int slot = page_slot(c, quad_position(r, x), off);
-  return __ldg(c.table + static_cast<size_t>(r.b) * c.max_pages + slot);
+  return __ldg(r.table + page_slot(c, oct_position(r, x), off));
 }
 
-// dt bits of a quad and which of its positions are seen (bit e of the result)
-__device__ __forceinline__ uint32_t load_quad(const PagedCache& c, const Row& r, int x, int page, uint32_t (&v)[4]) {
-  const int j0 = quad_position(r, x);
-  uint32_t seen = 0;
-  if ((c.page_size & 3) == 0) {
-    int off;
-    page_slot(c, j0, off);
+// dt bits of an oct; returns which of its positions are seen (bit e).  VEC: the
+// page size is a multiple of eight and dt_pages 32-byte aligned, so an oct lies
+// in one page and one 32-byte load brings it.
+template <bool VEC>
+__device__ __forceinline__ uint32_t load_oct(const PagedCache& c, const Row& r, int x, int page, uint32_t (&v)[8]) {
+  if (x >= r.no) return 0u;
+  const int j0 = oct_position(r, x);
+  uint32_t seen = oct_mask(r, x, j0);
+  int off;
+  int slot = page_slot(c, j0, off);
+  if (VEC) {
     page = checked_page(c, page);
-    if (page < 0) return 0;
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(c.dt_pages + dt_offset(c, page, off, r.g)));
-    v[0] = q.x;
-    v[1] = q.y;
-    v[2] = q.z;
-    v[3] = q.w;
+    if (page < 0) return 0u;
+    asm volatile("ld.global.nc.v8.u32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(c.dt_pages + dt_offset(c, page, off, r.g)));
+    return seen;
+  }
+  bool fresh = true;   // the page at hand has not been checked
 #pragma unroll
-    for (int e = 0; e < 4; ++e) seen |= quad_sees(r, x, j0 + e) ? 1u << e : 0u;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = 0;
-      if (!quad_sees(r, x, j0 + e)) continue;
-      int off;
-      const int slot = page_slot(c, j0 + e, off);
-      const int pg = checked_page(c, __ldg(c.table + static_cast<size_t>(r.b) * c.max_pages + slot));
-      if (pg < 0) continue;
-      v[e] = __float_as_uint(__ldg(c.dt_pages + dt_offset(c, pg, off, r.g)));
-      seen |= 1u << e;
+  for (int e = 0; e < 8; ++e) {
+    v[e] = 0u;
+    if (off == c.page_size) {
+      off = 0;
+      ++slot;
+      if (seen >> e) page = __ldg(r.table + slot);
+      fresh = true;
     }
+    if (seen >> e & 1u) {
+      if (fresh) page = checked_page(c, page);
+      fresh = false;
+      if (page < 0)
+        seen &= ~(1u << e);
+      else
+        v[e] = __float_as_uint(__ldg(c.dt_pages + dt_offset(c, page, off, r.g)));
+    }
+    ++off;
   }
   return seen;
 }
 
-// page of a quad where one entry covers it (else looked up per position)
-__device__ __forceinline__ int quad_page_or_none(const PagedCache& c, const Row& r, int x) {
-  return (c.page_size & 3) == 0 && x < r.nq ? quad_page(c, r, x) : 0;
-}
-
-__device__ __forceinline__ void write_entry(const PagedCache& c, const PagedLists& o, size_t at, const Row& r, uint64_t key) {
-  const int j = static_cast<int>(composite_index(key));
-  int off;
-  const int slot = page_slot(c, j, off);
-  const int page = __ldg(c.table + static_cast<size_t>(r.b) * c.max_pages + slot);   // checked when it was collected
-  o.row[at] = row_offset16(c, page, off, r.g);
-  o.bias[at] = __uint_as_float(static_cast<uint32_t>(key >> 32));
-}
+// A row's kept list.
+struct Kept {
+  int32_t* pos;
+  float* bias;
+  __device__ __forceinline__ void put(uint32_t at, int j, uint32_t bits) const {
+    pos[at] = j;
+    bias[at] = __uint_as_float(bits);
+  }
+  __device__ __forceinline__ void put(uint32_t at, uint64_t key) const {
+    put(at, static_cast<int>(composite_index(key)), static_cast<uint32_t>(key >> 32));
+  }
+};
 
 // Smallest shift that maps [0, range] into 2048 bins.
 __device__ __forceinline__ int bin_shift(uint32_t range) {
@@ -131,64 +151,133 @@ __device__ __forceinline__ int bin_shift(uint32_t range) {
   return top > 11 ? top - 11 : 0;
 }
 
+// Sum of the warps' values before this warp, from one value per warp.
+__device__ __forceinline__ uint32_t warps_before(const uint32_t* per_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  return __reduce_add_sync(0xFFFFFFFFu, lane < warp ? per_warp[lane] : 0u);
+}
+
+// The histogram bin (from the top) that holds the k-th key, how many of its
+// keys belong to the k, and how many it has; the histogram is cleared.  Every
+// thread calls it after a barrier behind the histogram's last addition and
+// gets the answer; `k` keys are there.  others: histograms of the cluster's
+// other CTAs to add.
+template <int THREADS, class F>
+__device__ __forceinline__ void top_bin(SpShared& sm, uint32_t k, F&& others, uint32_t& bin, uint32_t& need,
+                                        uint32_t& count) {
+  constexpr int PER = kBins / THREADS;   // bins per thread, the highest at thread 0
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int base = kBins - (tid + 1) * PER;
+  uint32_t h[PER], local = 0;
+#pragma unroll
+  for (int i = 0; i < PER; i += 2) {
+    uint2* mine = reinterpret_cast<uint2*>(sm.hist + base + i);
+    const uint2 x = *mine, y = others(base + i);
+    *mine = make_uint2(0u, 0u);
+    h[i] = x.x + y.x;
+    h[i + 1] = x.y + y.y;
+    local += h[i] + h[i + 1];
+  }
+  uint32_t above = local;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, above, d);
+    if (lane >= d) above += y;
+  }
+  if (lane == 31) sm.warp[0][warp] = above;
+  __syncthreads();
+  above += warps_before(sm.warp[0]) - local;
+  if (above < k && above + local >= k) {
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i) {
+      if (above < k && above + h[i] >= k) {
+        sm.bin[0] = static_cast<uint32_t>(base + i);
+        sm.bin[1] = k - above;
+        sm.bin[2] = h[i];
+      }
+      above += h[i];
+    }
+  }
+  __syncthreads();
+  bin = sm.bin[0];
+  need = sm.bin[1];
+  count = sm.bin[2];
+}
+
+// The rank in the sample whose key the w-th key of the row lies above but for
+// one row in a hundred thousand, when `expect` of the w best are sampled.
+template <class T>
+__host__ __device__ __forceinline__ T sample_rank(T expect) {
+  return expect + T(4.3) * sqrt(expect) + T(5);
+}
+
+struct NoOthers {
+  __device__ __forceinline__ uint2 operator()(int) const { return make_uint2(0u, 0u); }
+};
+
+// (count, minimum, maximum) over the block of each thread's own
+template <int THREADS>
+__device__ __forceinline__ void block_range(SpShared& sm, uint32_t& n, uint32_t& lo, uint32_t& hi) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  n = __reduce_add_sync(0xFFFFFFFFu, n);
+  lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+  hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+  if (lane == 0) {
+    sm.warp[0][warp] = n;
+    sm.warp[1][warp] = lo;
+    sm.warp[2][warp] = hi;
+  }
+  __syncthreads();
+  const bool in = lane < THREADS / 32;
+  n = __reduce_add_sync(0xFFFFFFFFu, in ? sm.warp[0][lane] : 0u);
+  lo = __reduce_min_sync(0xFFFFFFFFu, in ? sm.warp[1][lane] : 0xFFFFFFFFu);
+  hi = __reduce_max_sync(0xFFFFFFFFu, in ? sm.warp[2][lane] : 0u);
+}
+
 // Exact selection by one CTA: a few histogram passes over the row narrow the
 // dt bits of the w-th key to one value, then two passes write the keys above
 // it and the lowest-indexed ones equal to it.  Each warp owns a contiguous part
 // of the row, so the list is in a fixed order.
-static __device__ __noinline__ void select_exact(const PagedCache& c, const PagedLists& o, const Row& r, int w,
-                                                 SpSmem& sm) {
+template <int THREADS, bool VEC>
+static __device__ __noinline__ void select_exact(const PagedCache& c, const Kept& out, const Row& r, int w, SpShared& sm) {
+  constexpr int kWarps = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int seg = ((r.nq + kSpWarps - 1) / kSpWarps + 31) / 32 * 32;
-  const int x0 = min(r.nq, warp * seg), x1 = min(r.nq, x0 + seg);
-  const size_t base = (static_cast<size_t>(r.b) * c.Hkv + r.g) * o.cap;
-  auto each = [&](auto&& f) {   // f(quad, bits, seen): the whole warp calls it together
+  const int seg = ((r.no + kWarps - 1) / kWarps + 31) / 32 * 32;
+  const int x0 = min(r.no, warp * seg), x1 = min(r.no, x0 + seg);
+  auto each = [&](auto&& f) {   // f(oct, bits, seen): the whole warp calls it together
     for (int q0 = x0; q0 < x1; q0 += 32) {
       const int x = q0 + lane;
-      uint32_t v[4] = {0u, 0u, 0u, 0u};
-      const uint32_t seen = x < x1 ? load_quad(c, r, x, quad_page_or_none(c, r, x), v) : 0u;
+      uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      const uint32_t seen = x < x1 ? load_oct<VEC>(c, r, x, oct_page(c, r, x), v) : 0u;
       f(x, v, seen);
     }
   };
-  if (tid < 4) sm.stat[tid] = tid == 1 ? 0xFFFFFFFFu : 0u;   // [count, min, max]
-  __syncthreads();
-  {
-    uint32_t n = 0, lo = 0xFFFFFFFFu, hi = 0u;
-    each([&](int, const uint32_t(&v)[4], uint32_t seen) {
+  uint32_t total = 0, lo = 0xFFFFFFFFu, hi = 0u;
+  each([&](int, const uint32_t(&v)[8], uint32_t seen) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (seen >> e & 1u) {
-          ++n;
-          lo = min(lo, v[e]);
-          hi = max(hi, v[e]);
-        }
-    });
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-    if (lane == 0) {
-      atomicAdd(&sm.stat[0], n);
-      atomicMin(&sm.stat[1], lo);
-      atomicMax(&sm.stat[2], hi);
-    }
-  }
-  __syncthreads();
-  const uint32_t total = sm.stat[0];
-  uint32_t lo = sm.stat[1], hi = sm.stat[2];
+    for (int e = 0; e < 8; ++e)
+      if (seen >> e & 1u) {
+        ++total;
+        lo = min(lo, v[e]);
+        hi = max(hi, v[e]);
+      }
+  });
+  for (int i = tid; i < kBins; i += THREADS) sm.hist[i] = 0;
+  __syncthreads();   // what the caller left in shared memory has been read
+  block_range<THREADS>(sm, total, lo, hi);
   uint32_t k = static_cast<uint32_t>(w);   // keys to keep of those in [lo, hi]
   if (total > static_cast<uint32_t>(w)) {
     while (lo < hi) {
       const int s = bin_shift(hi - lo);
-      for (int i = tid; i < kBins; i += kSpThreads) sm.hist[i] = 0;
       __syncthreads();
-      each([&](int, const uint32_t(&v)[4], uint32_t seen) {
+      each([&](int, const uint32_t(&v)[8], uint32_t seen) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 8; ++e)
           if ((seen >> e & 1u) && v[e] >= lo && v[e] <= hi) atomicAdd(&sm.hist[(v[e] - lo) >> s], 1u);
       });
       __syncthreads();
-      uint32_t kin, cnt;
-      const uint32_t bin = find_bin_from_top(sm.hist, kBins, k, sm.red, sm.vars, &kin, &cnt);
-      k = kin;
+      uint32_t bin, cnt;
+      top_bin<THREADS>(sm, k, NoOthers{}, bin, k, cnt);
       const uint32_t l2 = lo + (bin << s);
       hi = min(hi, l2 + ((1u << s) - 1u));
       lo = l2;
@@ -200,139 +289,127 @@ static __device__ __noinline__ void select_exact(const PagedCache& c, const Page
   }
   // the keys above lo, then the k lowest-indexed ones equal to it
   uint32_t gt = 0, eq = 0;
-  each([&](int, const uint32_t(&v)[4], uint32_t seen) {
+  each([&](int, const uint32_t(&v)[8], uint32_t seen) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) {
       gt += (seen >> e & 1u) && v[e] > lo;
       eq += (seen >> e & 1u) && v[e] == lo;
     }
   });
   gt = __reduce_add_sync(0xFFFFFFFFu, gt);
   eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+  __syncthreads();
   if (lane == 0) {
-    sm.red[warp] = gt;
-    sm.red[16 + warp] = eq;
+    sm.warp[0][warp] = gt;
+    sm.warp[1][warp] = eq;
   }
   __syncthreads();
-  uint32_t gpos = 0, epos = 0, gall = 0;
-  for (int i = 0; i < kSpWarps; ++i) {
-    if (i < warp) {
-      gpos += sm.red[i];
-      epos += sm.red[16 + i];
-    }
-    gall += sm.red[i];
-  }
+  uint32_t gpos = warps_before(sm.warp[0]), epos = warps_before(sm.warp[1]);
+  const uint32_t gall = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? sm.warp[0][lane] : 0u);
   const uint32_t lt = lanemask_lt();
-  each([&](int x, const uint32_t(&v)[4], uint32_t seen) {
-    const int j0 = x < r.nq ? quad_position(r, x) : 0;
+  each([&](int x, const uint32_t(&v)[8], uint32_t seen) {
+    const int j0 = x < r.no ? oct_position(r, x) : 0;
     uint32_t n = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) n += (seen >> e & 1u) && v[e] == lo;
-    // this lane's first equal key's rank: prefix of n (0..4) over the lanes
+    for (int e = 0; e < 8; ++e) n += (seen >> e & 1u) && v[e] == lo;
+    // this lane's first equal key's rank: prefix of n (0..8) over the lanes
     const uint32_t b0 = __ballot_sync(0xFFFFFFFFu, n & 1u), b1 = __ballot_sync(0xFFFFFFFFu, n & 2u),
-                   b2 = __ballot_sync(0xFFFFFFFFu, n & 4u);
-    uint32_t er = epos + __popc(b0 & lt) + 2u * __popc(b1 & lt) + 4u * __popc(b2 & lt);
-    epos += __popc(b0) + 2u * __popc(b1) + 4u * __popc(b2);
+                   b2 = __ballot_sync(0xFFFFFFFFu, n & 4u), b3 = __ballot_sync(0xFFFFFFFFu, n & 8u);
+    uint32_t er = epos + __popc(b0 & lt) + 2u * __popc(b1 & lt) + 4u * __popc(b2 & lt) + 8u * __popc(b3 & lt);
+    epos += __popc(b0) + 2u * __popc(b1) + 4u * __popc(b2) + 8u * __popc(b3);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) {
       const bool above = (seen >> e & 1u) && v[e] > lo;
       const uint32_t vote = __ballot_sync(0xFFFFFFFFu, above);
-      if (above) write_entry(c, o, base + gpos + __popc(vote & lt), r, composite_key(v[e], j0 + e));
+      if (above) out.put(gpos + __popc(vote & lt), j0 + e, v[e]);
       gpos += __popc(vote);
       if ((seen >> e & 1u) && v[e] == lo) {
-        if (er < k) write_entry(c, o, base + gall + er, r, composite_key(v[e], j0 + e));
+        if (er < k) out.put(gall + er, j0 + e, v[e]);
         ++er;
       }
     }
   });
   // entries that pages outside the pool left empty
-  for (int e = static_cast<int>(min(total, static_cast<uint32_t>(w))) + tid; e < w; e += kSpThreads) {
-    o.row[base + e] = kNoRow;
-    o.bias[base + e] = 0.0f;
-  }
+  for (int e = static_cast<int>(min(total, static_cast<uint32_t>(w))) + tid; e < w; e += THREADS) out.put(e, -1, 0u);
 }
 
-__global__ void __launch_bounds__(kSpThreads, kSpMinBlocks)
-    select_paged_kernel(const __grid_constant__ PagedCache c, const __grid_constant__ PagedLists o) {
+// CLUSTER: a row's octs are dealt to the CTAs of a cluster (else it has one CTA).
+template <int THREADS, bool VEC, bool CLUSTER>
+__global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
+    select_paged_kernel(const __grid_constant__ PagedCache c, const __grid_constant__ PagedLists o, int room) {
+  using Cfg = SpCfg<THREADS>;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  SpSmem& sm = *reinterpret_cast<SpSmem*>(smem_raw);
+  SpShared& sm = *reinterpret_cast<SpShared*>(smem_raw);
+  uint64_t* lists = reinterpret_cast<uint64_t*>(smem_raw + sizeof(SpShared));
   cg::cluster_group cluster = cg::this_cluster();
+  auto sync_all = [&]() {
+    if (CLUSTER)
+      cluster.sync();
+    else
+      __syncthreads();
+  };
+  const int csize = CLUSTER ? static_cast<int>(cluster.num_blocks()) : 1;
+  const int rank = CLUSTER ? static_cast<int>(cluster.block_rank()) : 0;
+  auto of_rank = [&](int q) { return CLUSTER ? cluster.map_shared_rank(&sm, q) : &sm; };
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int csize = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int bg = blockIdx.x / csize;
-  const int b = bg / c.Hkv, g = bg % c.Hkv;
   const int w = c.w;
-  const SeqView view = seq_view(c, b);
+  const SeqView view = seq_view(c, bg / c.Hkv);
   if (view.n <= w) return;   // the attention takes such a row as it is (the whole cluster returns)
-  const Row r = make_row(c, view, b, g);
-  const size_t base = static_cast<size_t>(bg) * o.cap;
+  const Row r = make_row(c, view, bg / c.Hkv, bg % c.Hkv);
+  const Kept out{o.pos + static_cast<size_t>(bg) * o.cap, o.bias + static_cast<size_t>(bg) * o.cap};
 
   // ---- the sample and its threshold (every CTA of the cluster finds the same)
-  uint32_t* sample = reinterpret_cast<uint32_t*>(sm.keys);
-  const int squads = min(kSpSampleQuads, r.nq);
-  if (tid < 8) sm.stat[tid] = tid == 1 ? 0xFFFFFFFFu : 0u;   // [sampled, min, max, ...]
-  __syncthreads();
+  uint32_t* sample = reinterpret_cast<uint32_t*>(lists);
+  const int socts = min(view.n > kSpSampleLong ? kSpSample : kSpSample / 2, r.no);
+  for (int i = tid; i < kBins; i += THREADS) sm.hist[i] = 0;
+  if (tid == 0) sm.keys = sm.sure = sm.overflow = sm.edges = sm.exact = 0u;
+  uint32_t ns = 0, thr = 0xFFFFFFFFu, smax = 0u;
   {
-    constexpr int kPer = kSpSampleQuads / kSpThreads;
-    int page[kPer];
+    int at[Cfg::kSample], page[Cfg::kSample];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int s = i * kSpThreads + tid;
-      page[i] = s < squads ? quad_page_or_none(c, r, static_cast<int>(static_cast<long long>(s) * r.nq / squads)) : 0;
-    }
-    uint32_t n = 0, lo = 0xFFFFFFFFu, hi = 0u;
-    uint32_t v[kPer][4], seen[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int s = i * kSpThreads + tid;
-      seen[i] = s < squads ? load_quad(c, r, static_cast<int>(static_cast<long long>(s) * r.nq / squads), page[i], v[i])
-                           : 0u;
+    for (int i = 0; i < Cfg::kSample; ++i) {
+      const int s = i * THREADS + tid;
+      at[i] = s < socts ? static_cast<int>(static_cast<long long>(s) * r.no / socts) : r.no;
+      page[i] = oct_page(c, r, at[i]);
     }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int s = i * kSpThreads + tid;
+    for (int i = 0; i < Cfg::kSample; ++i) {
+      const int s = i * THREADS + tid;
+      if (s >= socts) continue;
+      uint32_t v[8];
+      const uint32_t seen = load_oct<VEC>(c, r, at[i], page[i], v);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool ok = seen[i] >> e & 1u;
-        if (s < squads) sample[4 * s + e] = ok ? v[i][e] : 0u;
+      for (int e = 0; e < 8; ++e) {
+        const bool ok = seen >> e & 1u;
+        sample[e * kSpSample + s] = ok ? v[e] : 0u;
         if (ok) {
-          ++n;
-          lo = min(lo, v[i][e]);
-          hi = max(hi, v[i][e]);
+          ++ns;
+          thr = min(thr, v[e]);
+          smax = max(smax, v[e]);
         }
       }
     }
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-    if (lane == 0) {
-      atomicAdd(&sm.stat[0], n);
-      atomicMin(&sm.stat[1], lo);
-      atomicMax(&sm.stat[2], hi);
-    }
   }
-  __syncthreads();
-  const uint32_t ns = sm.stat[0], smax = sm.stat[2];
-  uint32_t thr = sm.stat[1];
-  // the sample's rank that the w-th key of the row lies above but for one row in many thousands
-  const float expect = static_cast<float>(w) * static_cast<float>(ns) / static_cast<float>(view.n);
-  uint32_t k = static_cast<uint32_t>(expect + 4.0f * sqrtf(expect) + 5.0f);
+  block_range<THREADS>(sm, ns, thr, smax);
+  uint32_t k = static_cast<uint32_t>(
+      sample_rank(static_cast<float>(w) * static_cast<float>(ns) / static_cast<float>(view.n)));
   if (k < ns) {
     uint32_t lo = thr, hi = smax;
     while (lo < hi) {
       const int s = bin_shift(hi - lo);
-      for (int i = tid; i < kBins; i += kSpThreads) sm.hist[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < 4 * squads; i += kSpThreads) {
-        const uint32_t x = sample[i];   // unseen places hold 0: below lo, or the lowest value there is
-        if (x >= lo && x <= hi) atomicAdd(&sm.hist[(x - lo) >> s], 1u);
+      for (int q = tid; q < socts; q += THREADS) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t x = sample[e * kSpSample + q];   // unseen places hold 0: below lo, or the lowest value there is
+          if (x >= lo && x <= hi) atomicAdd(&sm.hist[(x - lo) >> s], 1u);
+        }
       }
       __syncthreads();
-      uint32_t kin, cnt;
-      const uint32_t bin = find_bin_from_top(sm.hist, kBins, k, sm.red, sm.vars, &kin, &cnt);
-      k = kin;
+      uint32_t bin, cnt;
+      top_bin<THREADS>(sm, k, NoOthers{}, bin, k, cnt);
       const uint32_t l2 = lo + (bin << s);
       hi = min(hi, l2 + ((1u << s) - 1u));
       lo = l2;
@@ -340,147 +417,143 @@ __global__ void __launch_bounds__(kSpThreads, kSpMinBlocks)
     }
     thr = lo;
   }
-  __syncthreads();   // the sample is read before keys are collected over it
+  __syncthreads();   // the sample has been read: entries are written over it
 
-  // ---- collect: 128-key chunks dealt to the cluster's warps in turn
-  uint32_t n_mine = 0;
-  uint64_t* mine = sm.keys[warp];
-  {
-    const int nchunk = (r.nq + 31) / 32, step = csize * kSpWarps;
-    const uint32_t lt = lanemask_lt();
-    int page[kSpChunks];
-    const int first = rank * kSpWarps + warp;
-#pragma unroll
-    for (int u = 0; u < kSpChunks; ++u) page[u] = quad_page_or_none(c, r, (first + u * step) * 32 + lane);
-    for (int c0 = first; c0 < nchunk; c0 += kSpChunks * step) {
-      uint32_t v[kSpChunks][4], seen[kSpChunks];
-#pragma unroll
-      for (int u = 0; u < kSpChunks; ++u) {
-        const int x = (c0 + u * step) * 32 + lane;
-        seen[u] = x < r.nq ? load_quad(c, r, x, page[u], v[u]) : 0u;
-      }
-#pragma unroll
-      for (int u = 0; u < kSpChunks; ++u)
-        page[u] = quad_page_or_none(c, r, (c0 + (kSpChunks + u) * step) * 32 + lane);
-#pragma unroll
-      for (int u = 0; u < kSpChunks; ++u) {
-        const int x = (c0 + u * step) * 32 + lane;
-        const int j0 = x < r.nq ? quad_position(r, x) : 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool take = (seen[u] >> e & 1u) && v[u][e] >= thr;
-          const uint32_t vote = __ballot_sync(0xFFFFFFFFu, take);
-          const uint32_t pos = n_mine + __popc(vote & lt);
-          if (take && pos < static_cast<uint32_t>(kSpRegion)) mine[pos] = composite_key(v[u][e], j0 + e);
-          n_mine += __popc(vote);
-        }
-      }
-    }
-  }
-  // ---- the w-th key's bin, over the cluster
+  // ---- collect, an oct per thread and step
   const int shift = bin_shift(smax > thr ? smax - thr : 0u);
   auto bin_of = [&](uint64_t key) {
     return min(static_cast<uint32_t>(kBins - 1), (static_cast<uint32_t>(key >> 32) - thr) >> shift);
   };
-  for (int i = tid; i < kBins; i += kSpThreads) sm.hist[i] = 0;
-  if (tid < 8) sm.stat[tid] = 0u;   // [0] overflow, [1] sure keys of this CTA, first CTA: [2] bin, [3] needed in it, [4] edge keys, [5] exact
-  __syncthreads();
-  if (lane == 0) {
-    sm.count[warp] = n_mine;
-    if (n_mine > static_cast<uint32_t>(kSpRegion)) sm.stat[0] = 1u;
-  }
-  for (uint32_t i = lane; i < min(n_mine, static_cast<uint32_t>(kSpRegion)); i += 32)
-    atomicAdd(&sm.hist[bin_of(mine[i])], 1u);
-  cluster.sync();
-  SpSmem* lead = cluster.map_shared_rank(&sm, 0);
-  if (rank == 0) {
-    uint32_t bad = sm.stat[0];
-    for (int q = 1; q < csize; ++q) {
-      SpSmem* other = cluster.map_shared_rank(&sm, q);
-      bad |= other->stat[0];
-      for (int i = tid; i < kBins; i += kSpThreads) sm.hist[i] += other->hist[i];
-    }
-    uint32_t mysum = 0;
-    for (int i = tid; i < kBins; i += kSpThreads) mysum += sm.hist[i];
-    uint32_t total;
-    block_exclusive_scan(mysum, sm.red, &total);
-    bad |= total < static_cast<uint32_t>(w);
-    if (!bad) {
-      uint32_t kin, cnt;
-      const uint32_t bin = find_bin_from_top(sm.hist, kBins, static_cast<uint32_t>(w), sm.red, sm.vars, &kin, &cnt);
-      bad = cnt > static_cast<uint32_t>(kSpEdge);
-      if (tid == 0) {
-        sm.stat[2] = bin;
-        sm.stat[3] = kin;
+  uint64_t* mine = lists + static_cast<size_t>(warp) * room;
+  uint32_t n = 0;   // keys of this warp
+  const uint32_t lt = lanemask_lt();
+  {
+    const int step = csize * THREADS;
+    int x = rank * THREADS + tid;
+    int page[Cfg::kUnroll];
+#pragma unroll
+    for (int u = 0; u < Cfg::kUnroll; ++u) page[u] = oct_page(c, r, x + u * step);
+    while (__any_sync(0xFFFFFFFFu, x < r.no)) {
+      uint32_t v[Cfg::kUnroll][8], seen[Cfg::kUnroll];
+#pragma unroll
+      for (int u = 0; u < Cfg::kUnroll; ++u) seen[u] = load_oct<VEC>(c, r, x + u * step, page[u], v[u]);
+#pragma unroll
+      for (int u = 0; u < Cfg::kUnroll; ++u) page[u] = oct_page(c, r, x + (Cfg::kUnroll + u) * step);
+#pragma unroll
+      for (int u = 0; u < Cfg::kUnroll; ++u) {
+        const uint32_t j0 = static_cast<uint32_t>(oct_position(r, x + u * step));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool take = (seen[u] >> e & 1u) && v[u][e] >= thr;
+          const uint32_t vote = __ballot_sync(0xFFFFFFFFu, take);
+          const uint32_t at = n + __popc(vote & lt);
+          if (take && at < static_cast<uint32_t>(room)) mine[at] = composite_key(v[u][e], j0 + e);
+          n += __popc(vote);
+        }
       }
+      x += Cfg::kUnroll * step;
     }
-    if (tid == 0) sm.stat[5] = bad;
+    if (lane == 0) {
+      if (n > static_cast<uint32_t>(room)) sm.overflow = 1u;
+      atomicAdd(&sm.keys, n);
+    }
+    n = min(n, static_cast<uint32_t>(room));
+    __syncwarp();
+    for (uint32_t i = lane; i < n; i += 32) atomicAdd(&sm.hist[bin_of(mine[i])], 1u);
   }
-  cluster.sync();
-  const uint32_t bad = lead->stat[5], wbin = lead->stat[2], need = lead->stat[3];
-  uint32_t sure = 0;
+
+  // ---- the w-th key's bin, over the cluster
+  sync_all();
+  uint32_t wbin, need, bad = 0, total = 0;
+  for (int q = 0; q < csize; ++q) {
+    const SpShared* other = of_rank(q);
+    bad |= other->overflow;
+    total += other->keys;
+  }
+  bad |= total < static_cast<uint32_t>(w);
+  SpShared* lead = of_rank(0);
+  if (!bad && rank == 0) {
+    uint32_t cnt;
+    top_bin<THREADS>(
+        sm, static_cast<uint32_t>(w),
+        [&](int i) {
+          uint2 s = make_uint2(0u, 0u);
+          for (int q = 1; q < csize; ++q) {
+            const uint2 y = *reinterpret_cast<const uint2*>(of_rank(q)->hist + i);
+            s.x += y.x;
+            s.y += y.y;
+          }
+          return s;
+        },
+        wbin, need, cnt);
+    if (tid == 0 && cnt > static_cast<uint32_t>(kSpEdge)) sm.exact = 1u;
+  }
+  sync_all();
+  wbin = lead->bin[0];
+  need = lead->bin[1];
+  bad |= lead->exact;
   if (!bad) {
     // keys inside the bin go to the first CTA (they are ranked by value, so
     // their order there does not matter); keys above it are counted
-    for (uint32_t i = lane; i < n_mine; i += 32) {
+    uint32_t sure = 0;
+    for (uint32_t i = lane; i < n; i += 32) {
       const uint64_t key = mine[i];
       const uint32_t bin = bin_of(key);
       sure += bin > wbin;
-      if (bin == wbin) lead->edge[atomicAdd(&lead->stat[4], 1u)] = key;
+      if (bin == wbin) lead->edge[atomicAdd(&lead->edges, 1u)] = key;
     }
     sure = __reduce_add_sync(0xFFFFFFFFu, sure);
     if (lane == 0) {
-      sm.count[warp] = sure;
-      atomicAdd(&sm.stat[1], sure);
+      sm.warp[1][warp] = sure;
+      atomicAdd(&sm.sure, sure);
     }
   }
-  cluster.sync();
+  sync_all();
   if (!bad) {
-    uint32_t pos = 0;
-    for (int q = 0; q < rank; ++q) pos += cluster.map_shared_rank(&sm, q)->stat[1];
-    for (int i = 0; i < warp; ++i) pos += sm.count[i];
-    const uint32_t lt = lanemask_lt();
-    for (uint32_t i0 = 0; i0 < n_mine; i0 += 32) {
-      const uint32_t i = i0 + lane;
-      const uint64_t key = i < n_mine ? mine[i] : 0ull;
-      const bool keep = i < n_mine && bin_of(key) > wbin;
+    uint32_t start = 0;
+    for (int q = 0; q < rank; ++q) start += of_rank(q)->sure;
+    uint32_t pos = start + warps_before(sm.warp[1]);
+    for (uint32_t i0 = 0; i0 < n; i0 += 32) {
+      const uint64_t key = i0 + lane < n ? mine[i0 + lane] : 0ull;
+      const bool keep = i0 + lane < n && bin_of(key) > wbin;
       const uint32_t vote = __ballot_sync(0xFFFFFFFFu, keep);
-      if (keep) write_entry(c, o, base + pos + __popc(vote & lt), r, key);
+      if (keep) out.put(pos + __popc(vote & lt), key);
       pos += __popc(vote);
     }
     if (rank == 0) {
       // the bin's `need` best keys, each at its rank
-      const uint32_t ne = sm.stat[4];
-      for (uint32_t i = tid; i < ne; i += kSpThreads) {
+      const uint32_t ne = sm.edges;
+      for (uint32_t i = tid; i < ne; i += THREADS) {
         const uint64_t key = sm.edge[i];
         uint32_t above = 0;
         for (uint32_t q = 0; q < ne; ++q) above += sm.edge[q] > key;
-        if (above < need) write_entry(c, o, base + (w - need) + above, r, key);
+        if (above < need) out.put(w - need + above, key);
       }
     }
   }
-  cluster.sync();   // no CTA leaves while another reads its shared memory
-  if (bad && rank == 0) select_exact(c, o, r, w, sm);
+  if (CLUSTER) cluster.sync();   // no CTA leaves while another reads its shared memory
+  if (bad && rank == 0) select_exact<THREADS, VEC>(c, out, r, w, sm);
 }
 
-}  // namespace
-
-cudaError_t launch_select_paged(const PagedCache& c, const PagedLists& lists, cudaStream_t s) {
-  constexpr int smem = static_cast<int>(sizeof(SpSmem));
-  cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(select_paged_kernel), smem);
+template <int THREADS, bool VEC, bool CLUSTER>
+cudaError_t launch_sp(const PagedCache& c, const PagedLists& lists, int rows, int csize, cudaStream_t s) {
+  // list entries per warp in the longest row the table can hold: its share of
+  // the keys expected above the threshold, and six standard deviations (of the
+  // threshold's rank in the sample, and of the share); larger windows than the
+  // bound allows are selected exactly
+  const double keys = static_cast<double>(c.max_pages) * c.page_size;
+  const double ratio = keys / (keys > kSpSampleLong ? 8.0 * kSpSample : 4.0 * kSpSample);   // keys per sampled one
+  const double rank = sample_rank(c.w / ratio);
+  const double share = rank * ratio * 32.0 / (static_cast<double>(THREADS) * csize);
+  const int room = static_cast<int>(std::min(share + 6.0 * std::sqrt(share + share * share / rank) + 8.0,
+                                             THREADS == 256 ? 2048.0 : 512.0));
+  const int smem = static_cast<int>(sizeof(SpShared)) + 8 * std::max(room * THREADS / 32, 4 * kSpSample);
+  const void* fn = reinterpret_cast<const void*>(select_paged_kernel<THREADS, VEC, CLUSTER>);
+  const cudaError_t e = ensure_dyn_smem(fn, smem);
   if (e != cudaSuccess) return e;
-  const int nsm = sm_count();
-  if (nsm <= 0) return cudaErrorInvalidDevice;
-  const int rows = c.B * c.Hkv;
-  // CTAs per row: while they fit on the SMs at once and each has 4096 keys of the
-  // longest row the table can hold
-  const long long keys = static_cast<long long>(c.max_pages) * c.page_size;
-  int csize = 1;
-  while (csize < 8 && 2LL * csize * rows <= static_cast<long long>(kSpMinBlocks) * nsm && keys >= 4096LL * 2 * csize)
-    csize *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows) * csize);
-  cfg.blockDim = dim3(kSpThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -491,8 +564,26 @@ cudaError_t launch_select_paged(const PagedCache& c, const PagedLists& lists, cu
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_paged_kernel, c, lists);
+  cfg.numAttrs = CLUSTER ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, select_paged_kernel<THREADS, VEC, CLUSTER>, c, lists, room);
+}
+
+}  // namespace
+
+cudaError_t launch_select_paged(const PagedCache& c, const PagedLists& lists, cudaStream_t s) {
+  const int nsm = sm_count();
+  if (nsm <= 0) return cudaErrorInvalidDevice;
+  const int rows = c.B * c.Hkv;
+  // CTAs per row: as many as the SMs hold at once, each with 4096 keys or more
+  // of the longest row the table can hold
+  const long long keys = static_cast<long long>(c.max_pages) * c.page_size;
+  int csize = 1;
+  while (csize < 8 && 2LL * csize * rows <= nsm && keys >= 4096LL * 2 * csize) csize *= 2;
+  const bool vec = c.page_size % 8 == 0 && (reinterpret_cast<uintptr_t>(c.dt_pages) & 31u) == 0;
+  if (csize > 1)
+    return vec ? launch_sp<1024, true, true>(c, lists, rows, csize, s)
+               : launch_sp<1024, false, true>(c, lists, rows, csize, s);
+  return vec ? launch_sp<256, true, false>(c, lists, rows, 1, s) : launch_sp<256, false, false>(c, lists, rows, 1, s);
 }
 
 }  // namespace dma

@@ -471,16 +471,16 @@ def decode_state_views(state, B, Lk, Hq, Hkv, d, keep_window_size):
 
 
 def paged_list_views(workspace, B, Hq, Hkv, d, keep_window_size):
-    """(row [B, Hkv, w] int64, bias [B, Hkv, w] float32) of a paged decode workspace with kept lists, for tests: a
-    key's row in 16-byte units of its pool (2^32 - 1: no key), and its dt.  Written for the rows that see more
-    than w keys."""
+    """(positions [B, Hkv, w] int32, bias [B, Hkv, w] float32) of a paged decode workspace with kept lists, for tests:
+    a kept key's position in its sequence (-1: no key), and its dt.  Written for the rows that see more than w keys.
+    The scratch of 256 blocks of eight warps lies before them."""
     def up(x):
         return -(-x // 256) * 256
     n = B * Hkv * keep_window_size * 4
-    off = up(256 + 2368 * 2 * (Hq // Hkv) * (d + 2) * 4)
-    row = workspace[off:off + n].view(torch.int32).long() & 0xFFFFFFFF
-    bias = workspace[up(off + n):up(off + n) + n].view(torch.float32)
-    return row.view(B, Hkv, keep_window_size), bias.view(B, Hkv, keep_window_size)
+    off = up(256 + 256 * 4 + 256 * 9 * 2 * (Hq // Hkv) * (d + 2) * 4)
+    shape = (B, Hkv, keep_window_size)
+    return (workspace[off:off + n].view(torch.int32).view(shape),
+            workspace[up(off + n):up(off + n) + n].view(torch.float32).view(shape))
 
 
 def dma_selftest_wait(workspace, stream=None):
