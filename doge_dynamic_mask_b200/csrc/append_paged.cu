@@ -305,7 +305,7 @@ cudaError_t launch_append(ApArgs a, const RopeTurns& turns, int nsm, cudaStream_
 }  // namespace
 
 cudaError_t launch_append_paged(const AppendPaged& p, uint32_t* err, cudaStream_t s) {
-  const RopeTurns turns = make_rope_turns(p.theta, p.d);
+  const RopeTurns& turns = make_rope_turns(p.theta, p.d);
   const int nsm = sm_count();
   if (nsm <= 0) return cudaErrorInvalidDevice;
   ApArgs a;

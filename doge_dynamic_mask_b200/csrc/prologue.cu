@@ -353,7 +353,7 @@ cudaError_t launch_prologue(const void* q, const void* k, const void* v, const f
   const long long tokens = static_cast<long long>(B) * L;
   if (tokens > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   if (d != 64 && d != 128) return cudaErrorInvalidValue;
-  const RopeTurns turns = make_rope_turns(theta, d);
+  const RopeTurns& turns = make_rope_turns(theta, d);
   const long long tbytes = static_cast<long long>(Hq + 2 * Hkv) * d * 2;   // one token's rows
   // tokens per stage: about 32 KB of rows (at most 16 tokens), three stages
   long long nts = kPrologueStageBytes / tbytes;

@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kPbReduceThreads)
 }  // namespace
 
 cudaError_t launch_prologue_backward(const PrologueBackward& p, cudaStream_t s) {
-  const RopeTurns turns = make_rope_turns(p.theta, p.d);
+  const RopeTurns& turns = make_rope_turns(p.theta, p.d);
   const int nsm = sm_count();
   if (nsm <= 0) return cudaErrorInvalidDevice;
   PbArgs a;

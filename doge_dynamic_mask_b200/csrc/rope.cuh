@@ -19,10 +19,18 @@ struct RopeTurns {
   double t[64];
 };
 
-inline RopeTurns make_rope_turns(float theta, int d) {
-  RopeTurns turns{};
-  const double log_theta = log(static_cast<double>(theta));
-  for (int i = 0; i < d / 2; ++i) turns.t[i] = exp(-2.0 * i / d * log_theta) * 0.15915494309189535;   // / (2 pi)
+// (the last table is kept per host thread: its 64 exponentials cost as much as
+// a third of a launch)
+inline const RopeTurns& make_rope_turns(float theta, int d) {
+  static thread_local RopeTurns turns{};
+  static thread_local float last_theta = 0.0f;
+  static thread_local int last_d = 0;
+  if (theta != last_theta || d != last_d) {
+    const double log_theta = log(static_cast<double>(theta));
+    for (int i = 0; i < d / 2; ++i) turns.t[i] = exp(-2.0 * i / d * log_theta) * 0.15915494309189535;   // / (2 pi)
+    last_theta = theta;
+    last_d = d;
+  }
   return turns;
 }
 

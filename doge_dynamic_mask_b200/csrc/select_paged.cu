@@ -8,9 +8,11 @@
 // Design.  One cluster of CTAs per (sequence, kv head).  The row is read once:
 // a sample (2048 keys, of long rows 4096, in runs of eight spread over the row)
 // gives a threshold that the w-th best key is above with four standard
-// deviations to spare, and every warp appends the keys at or above it that it
-// meets (about 1.6 w in all at 64k keys) to a list of its own in shared memory.
-// A histogram of the collected keys over the cluster finds the w-th key's bin;
+// deviations to spare, and every thread appends the keys at or above it that it
+// meets (about 1.6 w in all at 64k keys) to a list of its own in shared memory:
+// the pass is bound by integer instructions, and a list per warp, whose places
+// come from votes and population counts, took four times as many per key.  A
+// histogram of the collected keys over the cluster finds the w-th key's bin;
 // keys above the bin are kept, and the few inside are ranked one against
 // another by (dt, index).  The bound is the one read of dt plus the latency of
 // those steps; a row is spread over up to eight CTAs when there are fewer rows
@@ -34,25 +36,39 @@ namespace cg = cooperative_groups;
 constexpr int kSpSample = 512;           // sampled octs (runs of eight positions), at most
 constexpr int kSpSampleLong = 131072;    // rows up to this length take half of them
 constexpr int kSpEdge = 512;             // keys inside the w-th key's bin
-// many rows: 256 threads, four CTAs per SM; rows split over a cluster: 1024
+constexpr int kSpSpill = 128;            // keys of a CTA that found their thread's list full
+// many rows: 512 threads, two CTAs per SM; rows split over a cluster: 1024
 // threads, one CTA per SM
 template <int THREADS>
 struct SpCfg {
-  static constexpr int kMinBlocks = THREADS == 256 ? 4 : 1;
-  static constexpr int kSample = kSpSample > THREADS ? kSpSample / THREADS : 1;   // sampled octs per thread
-  static constexpr int kUnroll = 2;                                               // octs in flight per thread
+  static constexpr int kMinBlocks = THREADS == 512 ? 2 : 1;
+  static constexpr int kUnroll = 2;   // octs in flight per thread
+  static constexpr int kSlack = 4;    // list rows past the room: keys appended between two checks
 };
 
 struct SpShared {
   __align__(16) uint32_t hist[kBins];
   uint64_t edge[kSpEdge];                // (first CTA) keys inside the w-th key's bin
+  uint64_t spill[kSpSpill];              // keys that found their thread's list full
   uint32_t warp[3][32];                  // per-warp values
   uint32_t bin[3];                       // top_bin's answer
-  uint32_t keys, sure, overflow;         // this CTA's collected keys, those above the bin, lists that ran over
+  uint32_t keys, sure, spills;           // this CTA's collected keys, those above the bin, those in `spill`
   uint32_t edges, exact;                 // (first CTA) keys in `edge`; the row needs the exact selection
 };
-// dynamic shared memory: SpShared, then [warps][room] collected keys (the
-// sample's values before them)
+// dynamic shared memory: SpShared, then the collected keys' dt bits and
+// positions, [room + kSlack][2][THREADS] (first the sample's values)
+
+// Appends (bits, pos) at shared address `at` and moves it on, when bits reach
+// the threshold: four predicated instructions, no branch.
+template <int THREADS>
+__device__ __forceinline__ void append_if(uint32_t& at, uint32_t bits, uint32_t pos, uint32_t thr) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ge.u32 p, %1, %3;\n\t@p st.shared.u32 [%0], %1;\n\t@p st.shared.u32 [%0+%4], %2;\n\t"
+      "@p add.u32 %0, %0, %5;\n\t}"
+      : "+r"(at)
+      : "r"(bits), "r"(pos), "r"(thr), "n"(4 * THREADS), "n"(8 * THREADS)
+      : "memory");
+}
 
 // A row's visible keys as octs of eight positions: octs [0, noa) cover the
 // sinks, the rest the positions from `start` on.
@@ -84,19 +100,20 @@ __device__ __forceinline__ uint32_t oct_mask(const Row& r, int x, int j0) {
   return ((1u << min(8, max(0, hi - j0))) - 1u) & ~below;
 }
 
-// The table entry of an oct's first position (0 past the row).
-__device__ __forceinline__ int oct_page(const PagedCache& c, const Row& r, int x) {
-  if (x >= r.no) return 0;
+// The table entry of an oct's first position (0 from oct `end` on).
+__device__ __forceinline__ int oct_page(const PagedCache& c, const Row& r, int x, int end) {
+  if (x >= end) return 0;
   int off;
   return __ldg(r.table + page_slot(c, oct_position(r, x), off));
 }
 
 // dt bits of an oct; returns which of its positions are seen (bit e).  VEC: the
-// page size is a multiple of eight and dt_pages 32-byte aligned, so an oct lies
-// in one page and one 32-byte load brings it.
+// page size is a multiple of eight, so an oct lies in one page and two 16-byte
+// loads bring it.
 template <bool VEC>
-__device__ __forceinline__ uint32_t load_oct(const PagedCache& c, const Row& r, int x, int page, uint32_t (&v)[8]) {
-  if (x >= r.no) return 0u;
+__device__ __forceinline__ uint32_t load_oct(const PagedCache& c, const Row& r, int x, int page, uint32_t (&v)[8],
+                                             int end) {
+  if (x >= end) return 0u;
   const int j0 = oct_position(r, x);
   uint32_t seen = oct_mask(r, x, j0);
   int off;
@@ -104,9 +121,16 @@ __device__ __forceinline__ uint32_t load_oct(const PagedCache& c, const Row& r, 
   if (VEC) {
     page = checked_page(c, page);
     if (page < 0) return 0u;
-    asm volatile("ld.global.nc.v8.u32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "l"(c.dt_pages + dt_offset(c, page, off, r.g)));
+    const uint4* src = reinterpret_cast<const uint4*>(c.dt_pages + dt_offset(c, page, off, r.g));
+    const uint4 a = __ldg(src), b = __ldg(src + 1);
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = a.z;
+    v[3] = a.w;
+    v[4] = b.x;
+    v[5] = b.y;
+    v[6] = b.z;
+    v[7] = b.w;
     return seen;
   }
   bool fresh = true;   // the page at hand has not been checked
@@ -248,7 +272,7 @@ static __device__ __noinline__ void select_exact(const PagedCache& c, const Kept
     for (int q0 = x0; q0 < x1; q0 += 32) {
       const int x = q0 + lane;
       uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-      const uint32_t seen = x < x1 ? load_oct<VEC>(c, r, x, oct_page(c, r, x), v) : 0u;
+      const uint32_t seen = x < x1 ? load_oct<VEC>(c, r, x, oct_page(c, r, x, x1), v, x1) : 0u;
       f(x, v, seen);
     }
   };
@@ -340,7 +364,7 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
   using Cfg = SpCfg<THREADS>;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   SpShared& sm = *reinterpret_cast<SpShared*>(smem_raw);
-  uint64_t* lists = reinterpret_cast<uint64_t*>(smem_raw + sizeof(SpShared));
+  uint32_t* list = reinterpret_cast<uint32_t*>(smem_raw + sizeof(SpShared));
   cg::cluster_group cluster = cg::this_cluster();
   auto sync_all = [&]() {
     if (CLUSTER)
@@ -362,34 +386,24 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
   const Kept out{o.pos + static_cast<size_t>(bg) * o.cap, o.bias + static_cast<size_t>(bg) * o.cap};
 
   // ---- the sample and its threshold (every CTA of the cluster finds the same)
-  uint32_t* sample = reinterpret_cast<uint32_t*>(lists);
+  uint32_t* sample = list;
   const int socts = min(view.n > kSpSampleLong ? kSpSample : kSpSample / 2, r.no);
   for (int i = tid; i < kBins; i += THREADS) sm.hist[i] = 0;
-  if (tid == 0) sm.keys = sm.sure = sm.overflow = sm.edges = sm.exact = 0u;
+  if (tid == 0) sm.keys = sm.sure = sm.spills = sm.edges = sm.exact = 0u;
   uint32_t ns = 0, thr = 0xFFFFFFFFu, smax = 0u;
-  {
-    int at[Cfg::kSample], page[Cfg::kSample];
+  static_assert(THREADS >= kSpSample, "a sampled oct per thread, and the sample fits eight list rows");
+  if (tid < socts) {
+    const int x = static_cast<int>(static_cast<uint32_t>(tid * r.no) / static_cast<uint32_t>(socts));   // below 2^26
+    uint32_t v[8];
+    const uint32_t seen = load_oct<VEC>(c, r, x, oct_page(c, r, x, r.no), v, r.no);
 #pragma unroll
-    for (int i = 0; i < Cfg::kSample; ++i) {
-      const int s = i * THREADS + tid;
-      at[i] = s < socts ? static_cast<int>(static_cast<long long>(s) * r.no / socts) : r.no;
-      page[i] = oct_page(c, r, at[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < Cfg::kSample; ++i) {
-      const int s = i * THREADS + tid;
-      if (s >= socts) continue;
-      uint32_t v[8];
-      const uint32_t seen = load_oct<VEC>(c, r, at[i], page[i], v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool ok = seen >> e & 1u;
-        sample[e * kSpSample + s] = ok ? v[e] : 0u;
-        if (ok) {
-          ++ns;
-          thr = min(thr, v[e]);
-          smax = max(smax, v[e]);
-        }
+    for (int e = 0; e < 8; ++e) {
+      const bool ok = seen >> e & 1u;
+      sample[e * kSpSample + tid] = ok ? v[e] : 0u;
+      if (ok) {
+        ++ns;
+        thr = min(thr, v[e]);
+        smax = max(smax, v[e]);
       }
     }
   }
@@ -400,10 +414,10 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
     uint32_t lo = thr, hi = smax;
     while (lo < hi) {
       const int s = bin_shift(hi - lo);
-      for (int q = tid; q < socts; q += THREADS) {
+      if (tid < socts) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const uint32_t x = sample[e * kSpSample + q];   // unseen places hold 0: below lo, or the lowest value there is
+          const uint32_t x = sample[e * kSpSample + tid];   // unseen places hold 0: below lo, or the lowest value there is
           if (x >= lo && x <= hi) atomicAdd(&sm.hist[(x - lo) >> s], 1u);
         }
       }
@@ -417,49 +431,61 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
     }
     thr = lo;
   }
-  __syncthreads();   // the sample has been read: entries are written over it
+  __syncthreads();   // the sample has been read: keys are written over it
 
-  // ---- collect, an oct per thread and step
+  // ---- collect, an oct per thread and step.  Positions that are not seen read
+  // as 0, below any threshold; a threshold of 0 (dt that underflowed among the w
+  // best) is left to the exact selection.
   const int shift = bin_shift(smax > thr ? smax - thr : 0u);
-  auto bin_of = [&](uint64_t key) {
-    return min(static_cast<uint32_t>(kBins - 1), (static_cast<uint32_t>(key >> 32) - thr) >> shift);
-  };
-  uint64_t* mine = lists + static_cast<size_t>(warp) * room;
-  uint32_t n = 0;   // keys of this warp
-  const uint32_t lt = lanemask_lt();
-  {
-    const int step = csize * THREADS;
-    int x = rank * THREADS + tid;
+  auto bin_of = [&](uint32_t bits) { return min(static_cast<uint32_t>(kBins - 1), (bits - thr) >> shift); };
+  constexpr uint32_t kStep = 8u * THREADS;   // bytes between a thread's keys
+  const uint32_t first = smem_u32(list + tid);
+  const uint32_t full = first + static_cast<uint32_t>(room) * kStep;
+  uint32_t at = first;   // place of this thread's next key
+  if (thr > 0u) {
+    // each warp of the cluster takes a contiguous part of the row, 32 octs at a
+    // time, so that the list ends up roughly in the order of the positions
+    const int part = (r.no + csize * THREADS - 1) / (csize * THREADS) * 32;
+    const int xw = min(r.no, (rank * (THREADS / 32) + warp) * part), xe = min(r.no, xw + part);
     int page[Cfg::kUnroll];
 #pragma unroll
-    for (int u = 0; u < Cfg::kUnroll; ++u) page[u] = oct_page(c, r, x + u * step);
-    while (__any_sync(0xFFFFFFFFu, x < r.no)) {
+    for (int u = 0; u < Cfg::kUnroll; ++u) page[u] = oct_page(c, r, xw + lane + 32 * u, xe);
+    for (int x = xw + lane; x < xe; x += 32 * Cfg::kUnroll) {
       uint32_t v[Cfg::kUnroll][8], seen[Cfg::kUnroll];
 #pragma unroll
-      for (int u = 0; u < Cfg::kUnroll; ++u) seen[u] = load_oct<VEC>(c, r, x + u * step, page[u], v[u]);
+      for (int u = 0; u < Cfg::kUnroll; ++u) seen[u] = load_oct<VEC>(c, r, x + 32 * u, page[u], v[u], xe);
 #pragma unroll
-      for (int u = 0; u < Cfg::kUnroll; ++u) page[u] = oct_page(c, r, x + (Cfg::kUnroll + u) * step);
+      for (int u = 0; u < Cfg::kUnroll; ++u) page[u] = oct_page(c, r, x + 32 * (Cfg::kUnroll + u), xe);
 #pragma unroll
       for (int u = 0; u < Cfg::kUnroll; ++u) {
-        const uint32_t j0 = static_cast<uint32_t>(oct_position(r, x + u * step));
+        if (seen[u] != 255u) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const bool take = (seen[u] >> e & 1u) && v[u][e] >= thr;
-          const uint32_t vote = __ballot_sync(0xFFFFFFFFu, take);
-          const uint32_t at = n + __popc(vote & lt);
-          if (take && at < static_cast<uint32_t>(room)) mine[at] = composite_key(v[u][e], j0 + e);
-          n += __popc(vote);
+          for (int e = 0; e < 8; ++e) v[u][e] = seen[u] >> e & 1u ? v[u][e] : 0u;
+        }
+        const uint32_t j0 = static_cast<uint32_t>(oct_position(r, x + 32 * u));
+#pragma unroll
+        for (int e0 = 0; e0 < 8; e0 += Cfg::kSlack) {
+#pragma unroll
+          for (int e = e0; e < e0 + Cfg::kSlack; ++e) append_if<THREADS>(at, v[u][e], j0 + e, thr);
+          for (; at > full; at -= kStep) {   // the keys in the slack rows move to the CTA's spill
+            const uint32_t last = (at - first) / kStep - 1u;
+            const uint32_t bits = list[2 * last * THREADS + tid], pos = list[(2 * last + 1) * THREADS + tid];
+            const uint32_t i = atomicAdd(&sm.spills, 1u);
+            if (i < static_cast<uint32_t>(kSpSpill)) sm.spill[i] = composite_key(bits, pos);
+            atomicAdd(&sm.keys, 1u);
+            atomicAdd(&sm.hist[bin_of(bits)], 1u);
+          }
         }
       }
-      x += Cfg::kUnroll * step;
     }
-    if (lane == 0) {
-      if (n > static_cast<uint32_t>(room)) sm.overflow = 1u;
-      atomicAdd(&sm.keys, n);
-    }
-    n = min(n, static_cast<uint32_t>(room));
-    __syncwarp();
-    for (uint32_t i = lane; i < n; i += 32) atomicAdd(&sm.hist[bin_of(mine[i])], 1u);
+  }
+  const int n = static_cast<int>((at - first) / kStep);   // this thread's keys
+  auto key_bits = [&](int i) { return list[2 * i * THREADS + tid]; };
+  auto key_pos = [&](int i) { return static_cast<int>(list[(2 * i + 1) * THREADS + tid]); };
+  {
+    const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(n));
+    if (lane == 0) atomicAdd(&sm.keys, all);
+    for (int i = 0; i < n; ++i) atomicAdd(&sm.hist[bin_of(key_bits(i))], 1u);
   }
 
   // ---- the w-th key's bin, over the cluster
@@ -467,10 +493,10 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
   uint32_t wbin, need, bad = 0, total = 0;
   for (int q = 0; q < csize; ++q) {
     const SpShared* other = of_rank(q);
-    bad |= other->overflow;
+    bad |= other->spills > static_cast<uint32_t>(kSpSpill);
     total += other->keys;
   }
-  bad |= total < static_cast<uint32_t>(w);
+  bad |= total < static_cast<uint32_t>(w) || thr == 0u;
   SpShared* lead = of_rank(0);
   if (!bad && rank == 0) {
     uint32_t cnt;
@@ -492,42 +518,62 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
   wbin = lead->bin[0];
   need = lead->bin[1];
   bad |= lead->exact;
+  uint32_t before = 0;   // the warp's sure keys before this thread's
   if (!bad) {
     // keys inside the bin go to the first CTA (they are ranked by value, so
     // their order there does not matter); keys above it are counted
-    uint32_t sure = 0;
-    for (uint32_t i = lane; i < n; i += 32) {
-      const uint64_t key = mine[i];
-      const uint32_t bin = bin_of(key);
-      sure += bin > wbin;
+    for (int i = 0; i < n; ++i) {
+      const uint32_t bits = key_bits(i), bin = bin_of(bits);
+      before += bin > wbin;
+      if (bin == wbin) lead->edge[atomicAdd(&lead->edges, 1u)] = composite_key(bits, key_pos(i));
+    }
+    if (tid < sm.spills) {
+      const uint64_t key = sm.spill[tid];
+      const uint32_t bin = bin_of(static_cast<uint32_t>(key >> 32));
+      if (bin > wbin) atomicAdd(&sm.sure, 1u);
       if (bin == wbin) lead->edge[atomicAdd(&lead->edges, 1u)] = key;
     }
-    sure = __reduce_add_sync(0xFFFFFFFFu, sure);
-    if (lane == 0) {
-      sm.warp[1][warp] = sure;
-      atomicAdd(&sm.sure, sure);
+    const uint32_t own = before;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, before, d);
+      if (lane >= d) before += y;
     }
+    if (lane == 31) {
+      sm.warp[1][warp] = before;
+      atomicAdd(&sm.sure, before);
+    }
+    before -= own;
   }
   sync_all();
   if (!bad) {
     uint32_t start = 0;
     for (int q = 0; q < rank; ++q) start += of_rank(q)->sure;
-    uint32_t pos = start + warps_before(sm.warp[1]);
-    for (uint32_t i0 = 0; i0 < n; i0 += 32) {
-      const uint64_t key = i0 + lane < n ? mine[i0 + lane] : 0ull;
-      const bool keep = i0 + lane < n && bin_of(key) > wbin;
-      const uint32_t vote = __ballot_sync(0xFFFFFFFFu, keep);
-      if (keep) out.put(pos + __popc(vote & lt), key);
-      pos += __popc(vote);
+    uint32_t pos = start + warps_before(sm.warp[1]) + before;
+    for (int i = 0; i < n; ++i) {
+      const uint32_t bits = key_bits(i);
+      if (bin_of(bits) > wbin) out.put(pos++, static_cast<int>(key_pos(i)), bits);
+    }
+    // then the spilled ones, in the order of their positions
+    const uint32_t spills = sm.spills;
+    const uint64_t key = tid < spills ? sm.spill[tid] : 0ull;
+    auto is_sure = [&](uint64_t k) { return bin_of(static_cast<uint32_t>(k >> 32)) > wbin; };
+    if (spills > 0) {
+      pos = start + __reduce_add_sync(0xFFFFFFFFu, lane < THREADS / 32 ? sm.warp[1][lane] : 0u);
+      if (tid < spills && is_sure(key)) {
+        for (uint32_t i = 0; i < spills; ++i)
+          pos += is_sure(sm.spill[i]) && composite_index(sm.spill[i]) < composite_index(key);
+        out.put(pos, key);
+      }
     }
     if (rank == 0) {
       // the bin's `need` best keys, each at its rank
       const uint32_t ne = sm.edges;
       for (uint32_t i = tid; i < ne; i += THREADS) {
-        const uint64_t key = sm.edge[i];
+        const uint64_t mine = sm.edge[i];
         uint32_t above = 0;
-        for (uint32_t q = 0; q < ne; ++q) above += sm.edge[q] > key;
-        if (above < need) out.put(w - need + above, key);
+        for (uint32_t q = 0; q < ne; ++q) above += sm.edge[q] > mine;
+        if (above < need) out.put(w - need + above, mine);
       }
     }
   }
@@ -537,17 +583,19 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
 
 template <int THREADS, bool VEC, bool CLUSTER>
 cudaError_t launch_sp(const PagedCache& c, const PagedLists& lists, int rows, int csize, cudaStream_t s) {
-  // list entries per warp in the longest row the table can hold: its share of
-  // the keys expected above the threshold, and six standard deviations (of the
-  // threshold's rank in the sample, and of the share); larger windows than the
-  // bound allows are selected exactly
+  // list entries per thread in the longest row the table can hold: its share of
+  // the keys expected above the threshold, and four standard deviations (of the
+  // threshold's rank in the sample, and of the share; the few keys beyond spill);
+  // windows larger than shared memory holds are selected exactly
   const double keys = static_cast<double>(c.max_pages) * c.page_size;
   const double ratio = keys / (keys > kSpSampleLong ? 8.0 * kSpSample : 4.0 * kSpSample);   // keys per sampled one
   const double rank = sample_rank(c.w / ratio);
-  const double share = rank * ratio * 32.0 / (static_cast<double>(THREADS) * csize);
-  const int room = static_cast<int>(std::min(share + 6.0 * std::sqrt(share + share * share / rank) + 8.0,
-                                             THREADS == 256 ? 2048.0 : 512.0));
-  const int smem = static_cast<int>(sizeof(SpShared)) + 8 * std::max(room * THREADS / 32, 4 * kSpSample);
+  const double share = rank * ratio / (static_cast<double>(THREADS) * csize);
+  constexpr int kSlack = SpCfg<THREADS>::kSlack;
+  const int most = (226 * 1024 - static_cast<int>(sizeof(SpShared))) / (8 * THREADS) - kSlack;
+  const int room = std::max(8, static_cast<int>(std::min(share + 4.0 * std::sqrt(share + share * share / rank) + 2.0,
+                                                         static_cast<double>(most))));
+  const int smem = static_cast<int>(sizeof(SpShared)) + 8 * (room + kSlack) * THREADS;
   const void* fn = reinterpret_cast<const void*>(select_paged_kernel<THREADS, VEC, CLUSTER>);
   const cudaError_t e = ensure_dyn_smem(fn, smem);
   if (e != cudaSuccess) return e;
@@ -579,11 +627,11 @@ cudaError_t launch_select_paged(const PagedCache& c, const PagedLists& lists, cu
   const long long keys = static_cast<long long>(c.max_pages) * c.page_size;
   int csize = 1;
   while (csize < 8 && 2LL * csize * rows <= nsm && keys >= 4096LL * 2 * csize) csize *= 2;
-  const bool vec = c.page_size % 8 == 0 && (reinterpret_cast<uintptr_t>(c.dt_pages) & 31u) == 0;
+  const bool vec = c.page_size % 8 == 0;
   if (csize > 1)
     return vec ? launch_sp<1024, true, true>(c, lists, rows, csize, s)
                : launch_sp<1024, false, true>(c, lists, rows, csize, s);
-  return vec ? launch_sp<256, true, false>(c, lists, rows, 1, s) : launch_sp<256, false, false>(c, lists, rows, 1, s);
+  return vec ? launch_sp<512, true, false>(c, lists, rows, 1, s) : launch_sp<512, false, false>(c, lists, rows, 1, s);
 }
 
 }  // namespace dma

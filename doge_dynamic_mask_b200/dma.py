@@ -9,7 +9,6 @@ library has not been built.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import Optional
 
@@ -289,86 +288,110 @@ def dma_decode_step_cached(q, k_cache, v_cache, W_dt, A, lengths, keep_window_si
     return out
 
 
-def _tensor(name, t, dtype, shape, device, strided=False):
-    """Data pointer of an argument after checking what the library cannot see: its type, shape and device and,
-    unless the caller passes the strides on, that it is dense."""
-    if t.dtype is not dtype or t.device != device or t.shape != shape:
-        raise ValueError(f"{name}: {dtype} {tuple(shape)} on {device} is wanted, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if not strided and not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+# the current device and its current stream's handle, without building torch objects for them
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _elsewhere(call, device, stream, *args, **kw):
+    """The call with the stream it names, or its tensors' device, made current: what the binding allocates then
+    belongs to the stream that uses it."""
+    if device.type != "cuda":
+        raise ValueError("tensors passed to libdma must be CUDA tensors")
+    with torch.cuda.device(device) if stream is None else torch.cuda.stream(stream):
+        if _current_device() != device.index:
+            raise ValueError("the stream belongs to another device than the tensors")
+        return call(*args, **kw)
+
+
+def _refuse(device, *wanted):
+    """Names the argument that keeps a call from being made: (name, tensor, dtype, shape, may be strided)."""
+    for name, t, dtype, shape, strided in wanted:
+        if t is None:
+            continue
+        if t.dtype is not dtype or t.get_device() != device or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: {dtype} {tuple(shape)} on cuda:{device} is wanted, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        if not strided and not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+    raise ValueError("unsupported arguments")
 
 
 def _token_stride(name, t):
     """Elements between tokens of [.., H, d] whose head rows are dense (a slice of a wider projection's output)."""
-    d, st = t.shape[-1], t.stride()
-    if (st[-1] != 1 or (t.shape[-2] > 1 and st[-2] != d)
-            or (len(st) == 4 and t.shape[0] > 1 and st[0] != st[1] * t.shape[1])):
-        raise ValueError(f"{name}: its heads must be dense and its tokens evenly spaced")
-    if len(st) == 4 and t.shape[1] == 1:
-        return st[0] if t.shape[0] > 1 else t.shape[-2] * d
-    return st[-3] if t.shape[-3] > 1 else t.shape[-2] * d
+    shape, st = t.shape, t.stride()
+    d = shape[-1]
+    if st[-1] != 1 or (shape[-2] > 1 and st[-2] != d):
+        raise ValueError(f"{name}: its heads must be dense")
+    if len(st) == 3:
+        return st[0] if shape[0] > 1 else shape[1] * d
+    if shape[0] > 1 and shape[1] > 1 and st[0] != st[1] * shape[1]:
+        raise ValueError(f"{name}: its tokens must be evenly spaced")
+    return st[1] if shape[1] > 1 else st[0] if shape[0] > 1 else shape[2] * d
 
 
 def _page_stride(k_pages, v_pages):
     """Elements between the pages of both pools (the rest of a page is dense)."""
-    _, page_size, Hkv, d = k_pages.shape
+    _, page_size, Hkv, d = shape = k_pages.shape
     st = k_pages.stride()
-    if (k_pages.shape != v_pages.shape or st != v_pages.stride() or st[3] != 1 or (Hkv > 1 and st[2] != d)
+    if (v_pages.shape != shape or v_pages.stride() != st or st[3] != 1 or (Hkv > 1 and st[2] != d)
             or (page_size > 1 and st[1] != Hkv * d)):
         raise ValueError("k_pages and v_pages must have one shape and stride, with dense pages")
-    return st[0] if k_pages.shape[0] > 1 else page_size * Hkv * d
+    return st[0] if shape[0] > 1 else page_size * Hkv * d
 
 
-def _placed(call):
-    """Runs a binding with its first tensor's device current and, when a stream is given, on that stream: what it
-    allocates then belongs to the stream that uses it."""
-    @functools.wraps(call)
-    def placed(q, *args, stream=None, **kw):
-        if not q.is_cuda:
-            raise ValueError("tensors passed to libdma must be CUDA tensors")
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                return placed(q, *args, **kw)
-        if q.device.index != torch.cuda.current_device():
-            with torch.cuda.device(q.device):
-                return call(q, *args, **kw)
-        return call(q, *args, **kw)
-    return placed
-
-
-@_placed
 def dma_append_paged(q, k, v, q_norm_w, k_norm_w, W_dt, A, cu_tokens, positions, page_table, k_pages, v_pages,
-                     dt_pages, eps=1e-6, rope_theta=10000.0, q_out=None, k_out=None, workspace=None):
+                     dt_pages, eps=1e-6, rope_theta=10000.0, q_out=None, k_out=None, workspace=None, stream=None):
     """q/k RMSNorm and rotary embedding of a ragged batch's new tokens (packed [T, H, d]; sequence b owns tokens
     cu_tokens[b] .. cu_tokens[b + 1] - 1, at positions from positions[b] on), K and V to their pages, dt to
     dt_pages.  q, k and v may be slices of one projection's output.  Returns q_out; with k_out ([T, Hkv, d]) the
-    rotated K rows are written there too.  Takes `stream=` like every call here."""
+    rotated K rows are written there too."""
+    dev = q.get_device()
+    if dev < 0 or stream is not None or dev != _current_device():
+        return _elsewhere(dma_append_paged, q.device, stream, q, k, v, q_norm_w, k_norm_w, W_dt, A, cu_tokens,
+                          positions, page_table, k_pages, v_pages, dt_pages, eps, rope_theta, q_out, k_out, workspace)
     T, Hq, d = q.shape
     N, page_size, Hkv, _ = k_pages.shape
     B, max_pages = page_table.shape
-    dev, bf, f32, i32 = q.device, torch.bfloat16, torch.float32, torch.int32
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     if q_out is None:
-        q_out = torch.empty((T, Hq, d), dtype=bf, device=dev)
+        q_out = torch.empty((T, Hq, d), dtype=bf, device=q.device)
     if workspace is None:
-        workspace = new_workspace(256, dev)
-    page_stride = _page_stride(k_pages, v_pages)
+        workspace = new_workspace(256, q.device)
+    kv = (T, Hkv, d)
+    if not (q.dtype is bf and k.dtype is bf and v.dtype is bf and k_pages.dtype is bf and v_pages.dtype is bf
+            and q_out.dtype is bf and q_norm_w.dtype is f32 and k_norm_w.dtype is f32 and W_dt.dtype is f32
+            and A.dtype is f32 and dt_pages.dtype is f32 and cu_tokens.dtype is i32 and positions.dtype is i32
+            and page_table.dtype is i32 and k.shape == kv and v.shape == kv and q_out.shape == (T, Hq, d)
+            and k_pages.shape[3] == d and dt_pages.shape == (N, Hkv, page_size) and W_dt.shape == (Hkv * d, Hkv)
+            and q_norm_w.shape == k_norm_w.shape == (d,) and A.shape == (Hkv,) and cu_tokens.shape == (B + 1,)
+            and positions.shape == (B,)
+            and k.get_device() == v.get_device() == q_norm_w.get_device() == k_norm_w.get_device()
+            == W_dt.get_device() == A.get_device() == cu_tokens.get_device() == positions.get_device()
+            == page_table.get_device() == k_pages.get_device() == v_pages.get_device() == dt_pages.get_device()
+            == q_out.get_device() == workspace.get_device() == dev
+            and q_norm_w.is_contiguous() and k_norm_w.is_contiguous() and W_dt.is_contiguous() and A.is_contiguous()
+            and cu_tokens.is_contiguous() and positions.is_contiguous() and page_table.is_contiguous()
+            and dt_pages.is_contiguous() and q_out.is_contiguous() and workspace.is_contiguous()
+            and (k_out is None or (k_out.dtype is bf and k_out.shape == kv and k_out.get_device() == dev
+                                   and k_out.is_contiguous()))):
+        _refuse(dev, ("q", q, bf, (T, Hq, d), True), ("k", k, bf, kv, True), ("v", v, bf, kv, True),
+                ("q_norm_w", q_norm_w, f32, (d,), False), ("k_norm_w", k_norm_w, f32, (d,), False),
+                ("W_dt", W_dt, f32, (Hkv * d, Hkv), False), ("A", A, f32, (Hkv,), False),
+                ("cu_tokens", cu_tokens, i32, (B + 1,), False), ("positions", positions, i32, (B,), False),
+                ("page_table", page_table, i32, (B, max_pages), False),
+                ("k_pages", k_pages, bf, (N, page_size, Hkv, d), True),
+                ("v_pages", v_pages, bf, (N, page_size, Hkv, d), True),
+                ("dt_pages", dt_pages, f32, (N, Hkv, page_size), False), ("q_out", q_out, bf, (T, Hq, d), False),
+                ("k_out", k_out, bf, kv, False),
+                ("workspace", workspace, workspace.dtype, workspace.shape, False))
     _ok(_lib.dma_append_paged(
-        _tensor("q", q, bf, (T, Hq, d), dev, True), _tensor("k", k, bf, (T, Hkv, d), dev, True),
-        _tensor("v", v, bf, (T, Hkv, d), dev, True), _token_stride("q", q), _token_stride("k", k),
-        _token_stride("v", v), _tensor("q_norm_w", q_norm_w, f32, (d,), dev),
-        _tensor("k_norm_w", k_norm_w, f32, (d,), dev), eps, rope_theta,
-        _tensor("W_dt", W_dt, f32, (Hkv * d, Hkv), dev), _tensor("A", A, f32, (Hkv,), dev),
-        _tensor("cu_tokens", cu_tokens, i32, (B + 1,), dev), _tensor("positions", positions, i32, (B,), dev),
-        _tensor("page_table", page_table, i32, (B, max_pages), dev), T, B, max_pages, N, page_size, page_stride,
-        Hq, Hkv, d, _tensor("q_out", q_out, bf, (T, Hq, d), dev),
-        None if k_out is None else _tensor("k_out", k_out, bf, (T, Hkv, d), dev),
-        _tensor("k_pages", k_pages, bf, (N, page_size, Hkv, d), dev, True),
-        _tensor("v_pages", v_pages, bf, (N, page_size, Hkv, d), dev, True),
-        _tensor("dt_pages", dt_pages, f32, (N, Hkv, page_size), dev),
-        _tensor("workspace", workspace, torch.uint8, workspace.shape, dev), workspace.numel(),
-        torch.cuda.current_stream().cuda_stream), "dma_append_paged")
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _token_stride("q", q), _token_stride("k", k),
+        _token_stride("v", v), q_norm_w.data_ptr(), k_norm_w.data_ptr(), eps, rope_theta, W_dt.data_ptr(),
+        A.data_ptr(), cu_tokens.data_ptr(), positions.data_ptr(), page_table.data_ptr(), T, B, max_pages, N,
+        page_size, _page_stride(k_pages, v_pages), Hq, Hkv, d, q_out.data_ptr(),
+        None if k_out is None else k_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), dt_pages.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, _current_stream(dev)), "dma_append_paged")
     return q_out
 
 
@@ -377,34 +400,45 @@ def dma_decode_paged_workspace_size(B, max_pages, page_size, Hq, Hkv, d, keep_wi
                                                     sinks))
 
 
-@_placed
 def dma_decode_paged(q, k_pages, v_pages, dt_pages, page_table, lengths, keep_window_size, window=0, sinks=0,
-                     scale=None, out=None, workspace=None):
+                     scale=None, out=None, workspace=None, stream=None):
     """One new query per sequence ([B, Hq, d]) over a paged cache: of the keys a sequence of lengths[b] tokens
     sees (all, or the last `window` and the first `sinks`) the keep_window_size best by dt_pages, with dt as an
     additive bias.  A length of 0 gives a zero row."""
+    dev = q.get_device()
+    if dev < 0 or stream is not None or dev != _current_device():
+        return _elsewhere(dma_decode_paged, q.device, stream, q, k_pages, v_pages, dt_pages, page_table, lengths,
+                          keep_window_size, window, sinks, scale, out, workspace)
     B, Hq, d = q.shape
     N, page_size, Hkv, _ = k_pages.shape
     max_pages = page_table.shape[1]
-    dev, bf = q.device, torch.bfloat16
+    bf, i32 = torch.bfloat16, torch.int32
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty((B, Hq, d), dtype=bf, device=q.device)
     if workspace is None:
         size = dma_decode_paged_workspace_size(B, max_pages, page_size, Hq, Hkv, d, keep_window_size, window, sinks)
         if size == 0:
             raise ValueError("unsupported paged decode geometry")
-        workspace = new_workspace(size, dev)
-    page_stride = _page_stride(k_pages, v_pages)
+        workspace = new_workspace(size, q.device)
+    if not (q.dtype is bf and k_pages.dtype is bf and v_pages.dtype is bf and out.dtype is bf
+            and dt_pages.dtype is torch.float32 and page_table.dtype is i32 and lengths.dtype is i32
+            and out.shape == (B, Hq, d) and k_pages.shape[3] == d and dt_pages.shape == (N, Hkv, page_size)
+            and page_table.shape == (B, max_pages) and lengths.shape == (B,)
+            and k_pages.get_device() == v_pages.get_device() == dt_pages.get_device() == page_table.get_device()
+            == lengths.get_device() == out.get_device() == workspace.get_device() == dev
+            and q.is_contiguous() and dt_pages.is_contiguous() and page_table.is_contiguous()
+            and lengths.is_contiguous() and out.is_contiguous() and workspace.is_contiguous()):
+        _refuse(dev, ("q", q, bf, (B, Hq, d), False), ("k_pages", k_pages, bf, (N, page_size, Hkv, d), True),
+                ("v_pages", v_pages, bf, (N, page_size, Hkv, d), True),
+                ("dt_pages", dt_pages, torch.float32, (N, Hkv, page_size), False),
+                ("page_table", page_table, i32, (B, max_pages), False), ("lengths", lengths, i32, (B,), False),
+                ("out", out, bf, (B, Hq, d), False),
+                ("workspace", workspace, workspace.dtype, workspace.shape, False))
     _ok(_lib.dma_decode_paged(
-        _tensor("q", q, bf, (B, Hq, d), dev), _tensor("k_pages", k_pages, bf, (N, page_size, Hkv, d), dev, True),
-        _tensor("v_pages", v_pages, bf, (N, page_size, Hkv, d), dev, True),
-        _tensor("dt_pages", dt_pages, torch.float32, (N, Hkv, page_size), dev),
-        _tensor("page_table", page_table, torch.int32, (B, max_pages), dev),
-        _tensor("lengths", lengths, torch.int32, (B,), dev), B, max_pages, N, page_size, page_stride, Hq, Hkv, d,
-        keep_window_size, window, sinks, d ** -0.5 if scale is None else scale,
-        _tensor("out", out, bf, (B, Hq, d), dev),
-        _tensor("workspace", workspace, torch.uint8, workspace.shape, dev), workspace.numel(),
-        torch.cuda.current_stream().cuda_stream), "dma_decode_paged")
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), dt_pages.data_ptr(), page_table.data_ptr(),
+        lengths.data_ptr(), B, max_pages, N, page_size, _page_stride(k_pages, v_pages), Hq, Hkv, d,
+        keep_window_size, window, sinks, d ** -0.5 if scale is None else scale, out.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, _current_stream(dev)), "dma_decode_paged")
     return out
 
 
@@ -412,38 +446,55 @@ def dma_prologue_backward_workspace_size(B, L, Hq, Hkv, d) -> int:
     return int(_lib.dma_prologue_backward_workspace_size(B, L, Hq, Hkv, d))
 
 
-@_placed
 def dma_prologue_backward(q, k, q_norm_w, k_norm_w, positions, dq_out, dk_out, eps=1e-6, rope_theta=10000.0, dq=None,
-                          dk=None, dq_norm_w=None, dk_norm_w=None, workspace=None):
+                          dk=None, dq_norm_w=None, dk_norm_w=None, workspace=None, stream=None):
     """Gradients of dma_prologue's norms and rotation from those of its rotated q and k ([B, L, H, d]): returns
     (dq, dk) bf16 and (dq_norm_w, dk_norm_w) float32.  q, k, dq and dk may be slices of a projection's buffers."""
-    B, L, Hq, d = q.shape
+    dev = q.get_device()
+    if dev < 0 or stream is not None or dev != _current_device():
+        return _elsewhere(dma_prologue_backward, q.device, stream, q, k, q_norm_w, k_norm_w, positions, dq_out,
+                          dk_out, eps, rope_theta, dq, dk, dq_norm_w, dk_norm_w, workspace)
+    B, L, Hq, d = qs = q.shape
     Hkv = k.shape[2]
-    dev, bf, f32 = q.device, torch.bfloat16, torch.float32
+    ks = (B, L, Hkv, d)
+    bf, f32 = torch.bfloat16, torch.float32
     if dq is None:
-        dq = torch.empty((B, L, Hq, d), dtype=bf, device=dev)
+        dq = torch.empty(qs, dtype=bf, device=q.device)
     if dk is None:
-        dk = torch.empty((B, L, Hkv, d), dtype=bf, device=dev)
-    if dq_norm_w is None:
-        dq_norm_w = torch.empty(d, dtype=f32, device=dev)
-    if dk_norm_w is None:
-        dk_norm_w = torch.empty(d, dtype=f32, device=dev)
+        dk = torch.empty(ks, dtype=bf, device=q.device)
+    if dq_norm_w is None and dk_norm_w is None:
+        dq_norm_w, dk_norm_w = torch.empty((2, d), dtype=f32, device=q.device).unbind()
+    elif dq_norm_w is None or dk_norm_w is None:
+        raise ValueError("dq_norm_w and dk_norm_w: give both or neither")
     if workspace is None:
         size = dma_prologue_backward_workspace_size(B, L, Hq, Hkv, d)
         if size == 0:
             raise ValueError("unsupported prologue geometry")
-        workspace = new_workspace(size, dev)
+        workspace = new_workspace(size, q.device)
+    if not (q.dtype is bf and k.dtype is bf and dq_out.dtype is bf and dk_out.dtype is bf and dq.dtype is bf
+            and dk.dtype is bf and q_norm_w.dtype is f32 and k_norm_w.dtype is f32 and dq_norm_w.dtype is f32
+            and dk_norm_w.dtype is f32 and positions.dtype is torch.int32
+            and k.shape == dk_out.shape == dk.shape == ks and dq_out.shape == dq.shape == qs
+            and q_norm_w.shape == k_norm_w.shape == dq_norm_w.shape == dk_norm_w.shape == (d,)
+            and positions.shape == (B,)
+            and k.get_device() == dq_out.get_device() == dk_out.get_device() == dq.get_device() == dk.get_device()
+            == q_norm_w.get_device() == k_norm_w.get_device() == dq_norm_w.get_device() == dk_norm_w.get_device()
+            == positions.get_device() == workspace.get_device() == dev
+            and dq_out.is_contiguous() and dk_out.is_contiguous() and q_norm_w.is_contiguous()
+            and k_norm_w.is_contiguous() and dq_norm_w.is_contiguous() and dk_norm_w.is_contiguous()
+            and positions.is_contiguous() and workspace.is_contiguous()):
+        _refuse(dev, ("q", q, bf, qs, True), ("k", k, bf, ks, True), ("dq_out", dq_out, bf, qs, False),
+                ("dk_out", dk_out, bf, ks, False), ("dq", dq, bf, qs, True), ("dk", dk, bf, ks, True),
+                ("q_norm_w", q_norm_w, f32, (d,), False), ("k_norm_w", k_norm_w, f32, (d,), False),
+                ("dq_norm_w", dq_norm_w, f32, (d,), False), ("dk_norm_w", dk_norm_w, f32, (d,), False),
+                ("positions", positions, torch.int32, (B,), False),
+                ("workspace", workspace, workspace.dtype, workspace.shape, False))
     _ok(_lib.dma_prologue_backward(
-        _tensor("q", q, bf, (B, L, Hq, d), dev, True), _tensor("k", k, bf, (B, L, Hkv, d), dev, True),
-        _token_stride("q", q), _token_stride("k", k), _tensor("q_norm_w", q_norm_w, f32, (d,), dev),
-        _tensor("k_norm_w", k_norm_w, f32, (d,), dev), eps, rope_theta,
-        _tensor("positions", positions, torch.int32, (B,), dev), _tensor("dq_out", dq_out, bf, (B, L, Hq, d), dev),
-        _tensor("dk_out", dk_out, bf, (B, L, Hkv, d), dev), B, L, Hq, Hkv, d,
-        _tensor("dq", dq, bf, (B, L, Hq, d), dev, True), _tensor("dk", dk, bf, (B, L, Hkv, d), dev, True),
-        _token_stride("dq", dq), _token_stride("dk", dk), _tensor("dq_norm_w", dq_norm_w, f32, (d,), dev),
-        _tensor("dk_norm_w", dk_norm_w, f32, (d,), dev),
-        _tensor("workspace", workspace, torch.uint8, workspace.shape, dev), workspace.numel(),
-        torch.cuda.current_stream().cuda_stream), "dma_prologue_backward")
+        q.data_ptr(), k.data_ptr(), _token_stride("q", q), _token_stride("k", k), q_norm_w.data_ptr(),
+        k_norm_w.data_ptr(), eps, rope_theta, positions.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), B, L, Hq,
+        Hkv, d, dq.data_ptr(), dk.data_ptr(), _token_stride("dq", dq), _token_stride("dk", dk),
+        dq_norm_w.data_ptr(), dk_norm_w.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        _current_stream(dev)), "dma_prologue_backward")
     return dq, dk, dq_norm_w, dk_norm_w
 
 
