@@ -107,7 +107,7 @@ struct PagedLists {
 
 // Blocks that share a paged decode's work, at most (its scratch is sized for them).
 constexpr int kPagedMaxBlocks = 256;
-// Blocks of the prologue's backward, at most (a row of dw partials each).
+// Blocks of the prologue's backward, at most (a row of weight gradient shares each).
 constexpr int kPbMaxBlocks = 1024;
 
 // Arguments of the append to a paged cache and of the prologue's backward, as the entry points take them.
@@ -130,7 +130,8 @@ struct PrologueBackward {
   const void *dq_out, *dk_out;
   void *dq, *dk;
   long long dq_stride, dk_stride;
-  float *dq_norm_w, *dk_norm_w, *part;
+  float *dq_norm_w, *dk_norm_w;
+  void* scratch;                  // prologue_backward_scratch_bytes, zeroed before its first use
   float eps, theta;
   int B, L, Hq, Hkv, d;
 };
@@ -215,6 +216,7 @@ cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, cons
                               const void* v_pages, int Hq, float scale, void* scratch, void* out, cudaStream_t s);
 size_t attn_paged_scratch_bytes(int Hq, int Hkv, int d);
 cudaError_t launch_prologue_backward(const PrologueBackward& p, cudaStream_t s);
+size_t prologue_backward_scratch_bytes(int d);
 // CDMoE routing: router logits on the tensor cores (2K in {32, 64, 128, 256},
 // hidden a multiple of 64), then routing and experts (one CTA per token).
 cudaError_t launch_cdmoe_logits(const void* h, const void* W_router, int T, int hidden, int K, float* logits,

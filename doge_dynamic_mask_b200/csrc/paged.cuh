@@ -60,18 +60,6 @@ __device__ __forceinline__ uint32_t dt_offset(const PagedCache& c, int page, int
          static_cast<uint32_t>(g * c.page_size + off);
 }
 
-// Asynchronous copies to shared memory that write zeros where `there` is false
-// (the source is not read then).
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // a row offset that stands for no key
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 

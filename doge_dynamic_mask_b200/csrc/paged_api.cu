@@ -89,7 +89,7 @@ dma_status_t dma_append_paged(const void* q, const void* k, const void* v, int64
   if (!stride_ok(q_stride, Hq, d) || !stride_ok(k_stride, Hkv, d) || !stride_ok(v_stride, Hkv, d))
     return DMA_ERR_INVALID_ARG;
   if ((st = check_pages(B, max_pages, num_pages, page_size, page_stride, Hkv, d)) != DMA_OK) return st;
-  if (T > (1 << 30)) return DMA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(T) * Hq >= (1LL << 31)) return DMA_ERR_UNSUPPORTED;
   if (ws_bytes < kHeaderBytes) return DMA_ERR_WORKSPACE;
   if ((st = device_ok()) != DMA_OK) return st;
   const AppendPaged p{q,       k,         v,          q_stride,   k_stride,    v_stride, q_norm_w, k_norm_w,
@@ -151,8 +151,8 @@ dma_status_t dma_decode_paged(const void* q, const void* k_pages, const void* v_
 
 size_t dma_prologue_backward_workspace_size(int B, int L, int Hq, int Hkv, int d) {
   if (B < 1 || L < 1 || check_heads(Hq, Hkv, d) != DMA_OK) return 0;
-  if (static_cast<long long>(B) * L > (1LL << 30)) return 0;
-  return kHeaderBytes + static_cast<size_t>(kPbMaxBlocks) * 2 * d * 4;
+  if (static_cast<long long>(B) * L * Hq >= (1LL << 31)) return 0;
+  return kHeaderBytes + prologue_backward_scratch_bytes(d);
 }
 
 dma_status_t dma_prologue_backward(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
@@ -169,12 +169,12 @@ dma_status_t dma_prologue_backward(const void* q, const void* k, int64_t q_strid
   if (!stride_ok(q_stride, Hq, d) || !stride_ok(k_stride, Hkv, d) || !stride_ok(dq_stride, Hq, d) ||
       !stride_ok(dk_stride, Hkv, d))
     return DMA_ERR_INVALID_ARG;
-  if (static_cast<long long>(B) * L > (1LL << 30)) return DMA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * L * Hq >= (1LL << 31)) return DMA_ERR_UNSUPPORTED;
   if (ws_bytes < dma_prologue_backward_workspace_size(B, L, Hq, Hkv, d)) return DMA_ERR_WORKSPACE;
   if ((st = device_ok()) != DMA_OK) return st;
-  float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeaderBytes);
+  void* scratch = static_cast<char*>(workspace) + kHeaderBytes;
   const PrologueBackward p{q,  k,         q_stride,  k_stride,  q_norm_w,  k_norm_w, positions, dq_out, dk_out, dq,
-                           dk, dq_stride, dk_stride, dq_norm_w, dk_norm_w, part,     eps,       rope_theta, B,  L,
+                           dk, dq_stride, dk_stride, dq_norm_w, dk_norm_w, scratch,  eps,       rope_theta, B,  L,
                            Hq, Hkv,       d};
   const cudaError_t e = launch_prologue_backward(p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DMA_OK : cuda_fail(e);

@@ -16,14 +16,15 @@
 // flops per byte.  A row's channels sit in d/16 adjacent lanes, each with a
 // 16-byte chunk of channels i and the chunk of their partners i + d/2, so the
 // rotation needs no exchange and the two row sums are three shuffles or fewer.
-// A warp takes 32/(d/16) tokens at once, one per lane group, and walks over
-// the heads: the eight angles a lane needs are formed once per token and stay
-// in registers for all of its rows.  When there are fewer tokens than warps
-// the heads are split over warps too.  A lane always holds the same
-// channels, so its share of dw accumulates in float32 registers over
-// everything the warp does; the shares are added in a fixed order (lane
-// groups, then warps, then, in a second kernel, blocks), so the result does
-// not depend on timing.
+// A warp step takes four consecutive heads of a token (of two tokens at d = 64):
+// a contiguous piece of x, of g and of dx.  The eight angles a lane needs are
+// formed once per token.  The rows travel by cp.async through a ring in shared
+// memory in which each lane reads back only what it copied itself, so the steps
+// in flight need no registers or barriers.  A lane always holds the same
+// channels, so its share of dw accumulates in float32 registers over everything
+// the warp does; the shares are added in a fixed order (lane groups, warps,
+// blocks of a group, groups), so the result does not depend on timing; the last
+// block of a group, and the last group, add theirs, so there is no second launch.
 #include <algorithm>
 
 #include "rope.cuh"
@@ -31,10 +32,14 @@
 namespace dma {
 namespace {
 
-constexpr int kPbThreads = 256;
+constexpr int kPbThreads = 128;
 constexpr int kPbWarps = kPbThreads / 32;
-constexpr int kPbMinBlocks = 2;
-constexpr int kPbReduceThreads = 256;
+constexpr int kPbMinBlocks = 4;
+constexpr int kPbStages = 4;                                     // ring steps per warp
+constexpr int kPbGroup = 24;                                     // blocks whose shares are added first
+constexpr int kPbTicketBytes = 256;                               // kPbMaxBlocks / kPbGroup + 2 tickets
+static_assert((kPbMaxBlocks / kPbGroup + 2) * 4 <= kPbTicketBytes, "a ticket per group and one for the groups");
+constexpr int kPbSmemBytes = kPbWarps * kPbStages * 4 * 32 * 16;   // a step: four 16-byte chunks per lane
 
 struct PbArgs {
   const uint16_t *q, *k, *gq, *gk;
@@ -42,17 +47,18 @@ struct PbArgs {
   const float *q_w, *k_w;
   const int32_t* positions;
   uint16_t *dq, *dk;
-  float* part;         // [blocks][2][d]
+  float *dq_w, *dk_w;
+  float* part;         // [blocks][2][d], then [groups of blocks][2][d]
+  uint32_t* tickets;   // [groups + 1], zero between calls: finished blocks of a group; finished groups
   float eps;
-  int T, L, Hq, Hkv;
-  int splits;          // head splits per token group
+  int L;
+  RowShare share;
 };
 
 template <int D>
 __global__ void __launch_bounds__(kPbThreads, kPbMinBlocks)
     prologue_bwd_kernel(const __grid_constant__ PbArgs a, const __grid_constant__ RopeTurns turns) {
   constexpr int LPR = D / 16;          // lanes per row
-  constexpr int GPW = 32 / LPR;        // rows (tokens) per warp step
   constexpr int H = D / 2;
   __shared__ __align__(16) float s_w[2][D];
   __shared__ __align__(16) double s_turn[H];
@@ -67,72 +73,113 @@ __global__ void __launch_bounds__(kPbThreads, kPbMinBlocks)
   __syncthreads();
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int l = lane % LPR, grp = lane / LPR;
-  const int c0 = 8 * l;
-  const int rows = a.Hq + a.Hkv;
-  const int groups = (a.T + GPW - 1) / GPW;
-  const long long items = static_cast<long long>(groups) * a.splits;
+  const int c0 = 8 * (lane % LPR);
+  const int stride = static_cast<int>(gridDim.x) * kPbWarps;
+  const int it0 = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+  const int row0 = RowItem<D>::row();
+
+  // ---- the ring: rows of x and g on their way
+  extern __shared__ __align__(16) uint4 ring_all[];
+  uint4* ring = ring_all + warp * kPbStages * 128 + lane;   // [stage][x lo, x hi, g lo, g hi][lane]
+  const uint32_t ring_u = smem_u32(ring);
+  int f_it = it0, f_s = 0, f_h = 0, f_n = 0;
+  RowItem<D> f{};
+  const uint16_t *f_x = a.q, *f_g = a.gq;
+  auto f_tensor = [&](int n, int s) {   // step s is in tensor n
+    f_n = n;
+    f_h = 4 * s + row0;
+    const long long t = f.token;
+    f_x = (n ? a.k + t * a.k_stride : a.q + t * a.q_stride) + f_h * D + c0;
+    f_g = (n ? a.gk : a.gq) + (t * a.share.heads[n] + f_h) * D + c0;
+  };
+  auto f_enter = [&]() {
+    f.enter(a.share, f_it);
+    f_s = f.s0;
+    const int n = f_s >= a.share.q_steps;
+    f_tensor(n, n ? f_s - a.share.q_steps : f_s);
+  };
+  f_enter();
+  auto issue = [&](int slot) {
+    if (f_it < a.share.items) {
+      const bool there = f.there && f_h < a.share.heads[f_n];
+      const uint16_t *x = there ? f_x : a.q, *g = there ? f_g : a.gq;
+      const uint32_t dst = ring_u + slot * 2048;
+      cp_async16_zfill(dst, x, there);
+      cp_async16_zfill(dst + 512, x + H, there);
+      cp_async16_zfill(dst + 1024, g, there);
+      cp_async16_zfill(dst + 1536, g + H, there);
+      f_x += 4 * D;
+      f_g += 4 * D;
+      f_h += 4;
+      if (++f_s == f.s1) {
+        f_it += stride;
+        f_enter();
+      } else if (f_s == a.share.q_steps) {
+        f_tensor(1, 0);
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kPbStages - 1; ++s) issue(s);
+
   RowChunk dw[2];
 #pragma unroll
   for (int e = 0; e < 4; ++e) dw[0].lo[e] = dw[0].hi[e] = dw[1].lo[e] = dw[1].hi[e] = 0ull;
-
-  for (long long it = static_cast<long long>(warp) * gridDim.x + blockIdx.x; it < items;
-       it += static_cast<long long>(gridDim.x) * kPbWarps) {
-    const int tg = static_cast<int>(it / a.splits), part = static_cast<int>(it % a.splits);
-    const int h0 = static_cast<int>(static_cast<long long>(part) * rows / a.splits);
-    const int h1 = static_cast<int>(static_cast<long long>(part + 1) * rows / a.splits);
-    const int token = tg * GPW + grp;
-    const bool act = token < a.T;
-    const int b = act ? token / a.L : 0;
-    const double pos = act ? static_cast<double>(static_cast<long long>(a.positions[b]) + (token - b * a.L)) : 0.0;
-    const RowAngles ang = row_angles(pos, s_turn + c0);
-
-    // rows [ha, hb) of one tensor
-    auto walk = [&](int ha, int hb, const uint16_t* x, const uint16_t* g, uint16_t* dx, const float* w_s,
-                    RowChunk& acc) {
-      const RowChunk w = load_weights(w_s + c0, H);
-      const RawChunk zero{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-      RawChunk xr = act ? load_row(x + ha * D, H) : zero, gr = act ? load_row(g + ha * D, H) : zero;
-      for (int h = ha; h < hb; ++h) {
-        const RawChunk xc = xr, gc = gr;
-        if (act && h + 1 < hb) {   // the next row travels while this one is computed
-          xr = load_row(x + (h + 1) * D, H);
-          gr = load_row(g + (h + 1) * D, H);
-        }
-        RowChunk xh = widen_row(xc);
-        const float r = rsqrtf(row_sum<LPR>(chunk_dot(xh, xh)) * (1.0f / D) + a.eps);
-        const unsigned long long r2 = f32x2(r, r);
-        const RowChunk dy = rotate_row_back(widen_row(gc), ang);
-        RowChunk u;
+  int slot = 0;
+  RowItem<D> w;
+  for (int it = it0; it < a.share.items; it += stride) {
+    w.enter(a.share, it);
+    const int b = w.there ? w.token / a.L : 0;
+    const double pos =
+        w.there ? static_cast<double>(static_cast<long long>(a.positions[b]) + (w.token - b * a.L)) : 0.0;
+    const RowAngles ang = token_angles<D>(pos, s_turn);
+    // one row: its gradient to dx, its share of dw to acc
+    auto row = [&](bool act, uint16_t* dx, const float* w_s, RowChunk& acc) {
+      cp_wait<kPbStages - 2>();
+      const RawChunk xc{ring[slot * 128], ring[slot * 128 + 32]}, gc{ring[slot * 128 + 64], ring[slot * 128 + 96]};
+      issue(slot == 0 ? kPbStages - 1 : slot - 1);   // the step read last time
+      slot = slot + 1 == kPbStages ? 0 : slot + 1;
+      RowChunk xh = widen_row(xc);
+      const float r = rsqrtf(row_sum<LPR>(chunk_dot(xh, xh)) * (1.0f / D) + a.eps);
+      const unsigned long long r2 = f32x2(r, r);
+      RowChunk u = rotate_row_back(widen_row(gc), ang);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          xh.lo[e] = mul_f32x2(xh.lo[e], r2);
-          xh.hi[e] = mul_f32x2(xh.hi[e], r2);
-          acc.lo[e] = fma_f32x2(dy.lo[e], xh.lo[e], acc.lo[e]);
-          acc.hi[e] = fma_f32x2(dy.hi[e], xh.hi[e], acc.hi[e]);
-          u.lo[e] = mul_f32x2(dy.lo[e], w.lo[e]);
-          u.hi[e] = mul_f32x2(dy.hi[e], w.hi[e]);
-        }
-        const float m = -row_sum<LPR>(chunk_dot(u, xh)) * (1.0f / D);
-        const unsigned long long m2 = f32x2(m, m);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          u.lo[e] = mul_f32x2(fma_f32x2(xh.lo[e], m2, u.lo[e]), r2);
-          u.hi[e] = mul_f32x2(fma_f32x2(xh.hi[e], m2, u.hi[e]), r2);
-        }
-        if (act) store_row(dx + h * D, H, round_row(u));
+      for (int e = 0; e < 4; ++e) {
+        xh.lo[e] = mul_f32x2(xh.lo[e], r2);
+        xh.hi[e] = mul_f32x2(xh.hi[e], r2);
+        acc.lo[e] = fma_f32x2(u.lo[e], xh.lo[e], acc.lo[e]);
+        acc.hi[e] = fma_f32x2(u.hi[e], xh.hi[e], acc.hi[e]);
       }
+      const RowChunk wt = load_weights(w_s, H);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        u.lo[e] = mul_f32x2(u.lo[e], wt.lo[e]);
+        u.hi[e] = mul_f32x2(u.hi[e], wt.hi[e]);
+      }
+      const float m = -row_sum<LPR>(chunk_dot(u, xh)) * (1.0f / D);
+      const unsigned long long m2 = f32x2(m, m);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        u.lo[e] = mul_f32x2(fma_f32x2(xh.lo[e], m2, u.lo[e]), r2);
+        u.hi[e] = mul_f32x2(fma_f32x2(xh.hi[e], m2, u.hi[e]), r2);
+      }
+      if (act) store_row(dx, H, round_row(u));
     };
-    const long long t = token;
-    if (h0 < a.Hq)
-      walk(h0, min(h1, a.Hq), a.q + t * a.q_stride + c0, a.gq + t * a.Hq * D + c0, a.dq + t * a.dq_stride + c0,
-           s_w[0], dw[0]);
-    if (h1 > a.Hq)
-      walk(max(h0, a.Hq) - a.Hq, h1 - a.Hq, a.k + t * a.k_stride + c0, a.gk + t * a.Hkv * D + c0,
-           a.dk + t * a.dk_stride + c0, s_w[1], dw[1]);
+    const long long t = w.token;
+    const int q1 = min(w.s1, a.share.q_steps), k0 = max(w.s0, a.share.q_steps);
+    int h = 4 * w.s0 + row0;
+    uint16_t* dx = a.dq + t * a.dq_stride + h * D + c0;
+    for (int s = w.s0; s < q1; ++s, h += 4, dx += 4 * D)
+      row(w.there && h < a.share.heads[0], dx, s_w[0] + c0, dw[0]);
+    h = 4 * (k0 - a.share.q_steps) + row0;
+    dx = a.dk + t * a.dk_stride + h * D + c0;
+    for (int s = k0; s < w.s1; ++s, h += 4, dx += 4 * D)
+      row(w.there && h < a.share.heads[1], dx, s_w[1] + c0, dw[1]);
   }
+  cp_wait<0>();
 
-  // this block's share of the weight gradients: lane groups, then warps
+  // this warp's share of the weight gradients: the sum over its lane groups
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -144,9 +191,11 @@ __global__ void __launch_bounds__(kPbThreads, kPbMinBlocks)
       for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int o = LPR; o < 32; o <<= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
-        if (grp == 0) s_dw[warp][n][(i >= 2 ? H : 0) + c0 + 2 * e + (i & 1)] = v[i];
+        if (lane < LPR) s_dw[warp][n][(i >= 2 ? H : 0) + c0 + 2 * e + (i & 1)] = v[i];
       }
     }
+
+  // the block's share: its warps in order
   __syncthreads();
   for (int c = threadIdx.x; c < 2 * D; c += kPbThreads) {
     float s = 0.0f;
@@ -154,31 +203,41 @@ __global__ void __launch_bounds__(kPbThreads, kPbMinBlocks)
     for (int w = 0; w < kPbWarps; ++w) s += s_dw[w][c / D][c % D];
     a.part[static_cast<size_t>(blockIdx.x) * 2 * D + c] = s;
   }
-}
-
-// Sum of the blocks' shares, 32 channels per block: each warp adds every eighth
-// block's row in order, then the warps' sums are added in order.
-__global__ void __launch_bounds__(kPbReduceThreads)
-    prologue_bwd_reduce_kernel(const float* part, int blocks, int d, float* __restrict__ dq_w,
-                               float* __restrict__ dk_w) {
-  constexpr int kWarps = kPbReduceThreads / 32;
-  __shared__ float s[kWarps][32];
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x * 32 + lane;
-  float v = 0.0f;
+  // the last block of a group adds the group's shares, the last group all of them
+  const int blocks = static_cast<int>(gridDim.x), groups = (blocks + kPbGroup - 1) / kPbGroup;
+  const int group = static_cast<int>(blockIdx.x) / kPbGroup;
+  __shared__ bool s_last;
+  auto last_of = [&](uint32_t* ticket, int n) {   // whether this block is the n-th to take the ticket
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      __threadfence();
+      s_last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(n - 1);
+      if (s_last) *ticket = 0u;
+      __threadfence();
+    }
+    __syncthreads();
+    return s_last;
+  };
+  auto add = [&](const float* rows, int n, int c) {
+    float s = 0.0f;
 #pragma unroll 8
-  for (int b = warp; b < blocks; b += kWarps) v += part[static_cast<size_t>(b) * 2 * d + c];
-  s[warp][lane] = v;
-  __syncthreads();
-  if (warp == 0) {
-    float t = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) t += s[w][lane];
-    if (c < d)
-      dq_w[c] = t;
+    for (int i = 0; i < n; ++i) s += __ldcg(rows + static_cast<size_t>(i) * 2 * D + c);
+    return s;
+  };
+  const int in_group = min(kPbGroup, blocks - group * kPbGroup);
+  float* sums = a.part + static_cast<size_t>(blocks) * 2 * D;
+  if (!last_of(a.tickets + group, in_group)) return;
+  for (int c = threadIdx.x; c < 2 * D; c += kPbThreads) {
+    const float s = add(a.part + static_cast<size_t>(group) * kPbGroup * 2 * D, in_group, c);
+    sums[static_cast<size_t>(group) * 2 * D + c] = s;
+  }
+  if (!last_of(a.tickets + groups, groups)) return;
+  for (int c = threadIdx.x; c < 2 * D; c += kPbThreads) {
+    const float s = add(sums, groups, c);
+    if (c < D)
+      a.dq_w[c] = s;
     else
-      dk_w[c - d] = t;
+      a.dk_w[c - D] = s;
   }
 }
 
@@ -202,26 +261,24 @@ cudaError_t launch_prologue_backward(const PrologueBackward& p, cudaStream_t s) 
   a.positions = p.positions;
   a.dq = static_cast<uint16_t*>(p.dq);
   a.dk = static_cast<uint16_t*>(p.dk);
-  a.part = p.part;
+  a.dq_w = p.dq_norm_w;
+  a.dk_w = p.dk_norm_w;
+  a.tickets = static_cast<uint32_t*>(p.scratch);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(p.scratch) + kPbTicketBytes);
   a.eps = p.eps;
-  a.T = p.B * p.L;
   a.L = p.L;
-  a.Hq = p.Hq;
-  a.Hkv = p.Hkv;
-  // tokens are taken in groups of 4 (d = 128) or 8 (d = 64) per warp; with
-  // fewer groups than resident warps the heads of a token are split as well
-  const int gpw = 32 / (p.d / 16);
-  const long long groups = (static_cast<long long>(a.T) + gpw - 1) / gpw;
-  const long long slots = static_cast<long long>(std::min(kPbMinBlocks * nsm, kPbMaxBlocks)) * kPbWarps;
-  a.splits = static_cast<int>(std::max(1LL, std::min<long long>(p.Hq + p.Hkv, slots / groups)));
-  const long long items = groups * a.splits;
+  const int slots = std::min(kPbMinBlocks * nsm, kPbMaxBlocks);
+  a.share = share_rows(p.B * p.L, p.Hq, p.Hkv, p.d, static_cast<long long>(slots) * kPbWarps);
   // few items spread over blocks (and SMs) before they share one
-  const int blocks = static_cast<int>(std::min<long long>(items, slots / kPbWarps));
-  cudaError_t e = p.d == 64 ? launch_after(prologue_bwd_kernel<64>, dim3(blocks), dim3(kPbThreads), 0, s, a, turns)
-                            : launch_after(prologue_bwd_kernel<128>, dim3(blocks), dim3(kPbThreads), 0, s, a, turns);
+  const int blocks = std::min(a.share.items, slots);
+  auto* kernel = p.d == 64 ? prologue_bwd_kernel<64> : prologue_bwd_kernel<128>;
+  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), kPbSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_after(prologue_bwd_reduce_kernel, dim3(2 * p.d / 32), dim3(kPbReduceThreads), 0, s, p.part, blocks, p.d,
-                      p.dq_norm_w, p.dk_norm_w);
+  return launch_after(kernel, dim3(blocks), dim3(kPbThreads), kPbSmemBytes, s, a, turns);
+}
+
+size_t prologue_backward_scratch_bytes(int d) {
+  return kPbTicketBytes + static_cast<size_t>(kPbMaxBlocks + kPbMaxBlocks / kPbGroup + 1) * 2 * d * sizeof(float);
 }
 
 }  // namespace dma

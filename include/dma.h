@@ -320,11 +320,11 @@ DMA_API dma_status_t dma_decode_step_cached(const void* q, const void* k_cache, 
  *   dq_out, dk_out  [B, L, Hq, d], [B, L, Hkv, d] bf16, dense
  *   dq, dk        as q and k, with dq_stride and dk_stride (written)
  *   dq_norm_w, dk_norm_w  [d] float32 (written, not added to)
- *   workspace     dma_prologue_backward_workspace_size(...) bytes
+ *   workspace     dma_prologue_backward_workspace_size(...) bytes, zeroed once
  * Strides are multiples of 8, at least heads * d.  Outputs must not overlap
  * inputs.  The weight gradients' terms are added in a fixed order: the same call
  * gives the same bits.  Supported: d in {64, 128}, Hkv in {1, 2, 4, 8, 16},
- * Hq a multiple of Hkv, Hq / Hkv <= 8, B * L <= 2^30.
+ * Hq a multiple of Hkv, Hq / Hkv <= 8, B * L * Hq < 2^31.
  */
 DMA_API size_t dma_prologue_backward_workspace_size(int B, int L, int Hq, int Hkv, int d);
 DMA_API dma_status_t dma_prologue_backward(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
@@ -363,7 +363,7 @@ DMA_API dma_status_t dma_prologue_backward(const void* q, const void* k, int64_t
  *                 cu_tokens[B] on (padding of a captured batch) are ignored and their
  *                 q_out and k_out rows stay as they are
  *   positions     [B] int32: tokens each sequence has cached before
- *   T             tokens in the packed tensors, at most 2^30
+ *   T             tokens in the packed tensors (T * Hq < 2^31)
  *   q_out         [T, Hq, d] bf16 (written)
  *   k_out         [T, Hkv, d] bf16 or NULL: the normalised and rotated K rows too, packed
  *                 (for dma_forward_prefill over a prompt)
