@@ -121,8 +121,19 @@ struct KeyPage {
 // before the range, slot 1 one that begins in it and goes on.
 enum : int { kNone = 0, kEnds = 1, kThrough = 2, kOpen = 3 };
 struct RowCut {
-  long long t0;      // the row's first tile on the axis
+  uint32_t t0;       // the row's first tile on the axis
   int nt, b, g;
+};
+
+// The axis of U tiles (32 bits hold it: the entry point refuses more) over G
+// blocks: the first U % G of them have a tile more than the others.
+struct Axis {
+  uint32_t per, more, split;   // tiles of a late block; blocks with one more; where the late ones begin
+  __device__ __forceinline__ Axis(uint32_t U, uint32_t G) : per(U / G), more(U - U / G * G) { split = more * (per + 1u); }
+  __device__ __forceinline__ uint32_t begin(uint32_t block) const { return block * per + min(block, more); }
+  __device__ __forceinline__ uint32_t block_of(uint32_t tile) const {
+    return tile < split ? tile / (per + 1u) : more + (tile - split) / per;
+  }
 };
 
 // Joins n pieces of a row for four channels of a head: piece(i) points at
@@ -162,7 +173,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
   constexpr int RPI = 32 / CPR;         // rows per copy step of a warp
   constexpr int STG = Cfg::kStages;
   extern __shared__ __align__(128) unsigned char ring_all[];
-  __shared__ long long s_pref[kDpThreads];     // tiles of the sequences up to and with this one
+  __shared__ uint32_t s_pref[kDpThreads];      // tiles of the sequences up to and with this one
   __shared__ uint32_t s_warp[kDpWarps];
   __shared__ RowCut s_cut[kDpWarps][2];
   __shared__ int s_kind[kDpWarps][2];
@@ -173,7 +184,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // ---- the axis: U tiles; G blocks take at least a tile per warp
-  auto scan_step = [&](int b0, long long before) {   // over sequences [b0, b0 + kDpThreads)
+  auto scan_step = [&](int b0, uint32_t before) {   // over sequences [b0, b0 + kDpThreads)
     uint32_t x = b0 + tid < c.B ? static_cast<uint32_t>(seq_tiles(c, b0 + tid)) : 0u;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -192,20 +203,22 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
     s_pref[tid] = before + x;
     return before + all;
   };
-  long long total = 0;
+  uint32_t total = 0;
   for (int b0 = 0; b0 < c.B; b0 += kDpThreads) total = scan_step(b0, total);
-  const long long U = total * c.Hkv;
-  const long long G = min(static_cast<long long>(gridDim.x), (U + kDpWarps - 1) / kDpWarps);
-  if (static_cast<long long>(blockIdx.x) >= G) return;
-  const long long xb0 = U * blockIdx.x / G, xb1 = U * (blockIdx.x + 1LL) / G;
-  const long long x0 = xb0 + (xb1 - xb0) * warp / kDpWarps, x1 = xb0 + (xb1 - xb0) * (warp + 1) / kDpWarps;
-  const int count = static_cast<int>(x1 - x0);
+  const uint32_t U = total * static_cast<uint32_t>(c.Hkv);
+  const uint32_t G = min(gridDim.x, (U + kDpWarps - 1u) / kDpWarps);
+  if (blockIdx.x >= G) return;
+  const Axis axis(U, G);
+  const uint32_t xb0 = axis.begin(blockIdx.x), xb1 = axis.begin(blockIdx.x + 1u), nb = xb1 - xb0;
+  auto warp_begin = [&](uint32_t w) { return xb0 + nb * w / kDpWarps; };
+  const uint32_t x0 = warp_begin(warp);
+  const int count = static_cast<int>(warp_begin(warp + 1) - x0);
   Cursor cur{};
   {
-    const long long y = x0 / c.Hkv;   // tiles of sequences before x0's, rounded into it
-    long long before = 0;
+    const uint32_t y = x0 >> (31 - __clz(c.Hkv));   // (Hkv is a power of two) tiles of sequences before x0's, rounded into it
+    uint32_t before = 0;
     for (int b0 = 0; b0 < c.B; b0 += kDpThreads) {
-      const long long next = c.B > kDpThreads ? scan_step(b0, before) : total;
+      const uint32_t next = c.B > kDpThreads ? scan_step(b0, before) : total;
       __syncthreads();
       if (y >= before && y < next) {
         int n = 0;   // sequences of this step that end at or before y
@@ -213,9 +226,9 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
         for (int i = 0; i < kDpThreads; i += 32) n += __popc(__ballot_sync(0xFFFFFFFFu, s_pref[i + lane] <= y));
         cur.b = b0 + n;
         cur.enter(c);
-        const long long rem = x0 - (n > 0 ? s_pref[n - 1] : before) * c.Hkv;
-        cur.g = static_cast<int>(rem / cur.nt);
-        cur.t = static_cast<int>(rem % cur.nt);
+        const uint32_t rem = x0 - (n > 0 ? s_pref[n - 1] : before) * static_cast<uint32_t>(c.Hkv);
+        cur.g = static_cast<int>(rem / static_cast<uint32_t>(cur.nt));
+        cur.t = static_cast<int>(rem) - cur.g * cur.nt;
       }
       before = next;
     }
@@ -259,13 +272,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
     return e;
   };
   const int cr = lane / CPR, cc = lane % CPR;
-  KeyPos npos = position();
-  KeyPage next = entry(npos);
-  npos = position();
-  auto issue = [&](int slot) {   // the tile whose entries came last; then the next one's
-    const KeyPage k = next;
-    next = entry(npos);
-    npos = position();
+  auto issue = [&](const KeyPage& k, int slot) {
     const int page = k.off >= 0 ? checked_page(c, k.page) : -1;
     const uint32_t krow = page >= 0 ? row_offset16(c, page, k.off, k.g) : kNoRow;
     const float* dt = page < 0 ? c.dt_pages : k.dt ? k.dt : c.dt_pages + dt_offset(c, page, k.off, k.g);
@@ -286,10 +293,24 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
       cp_async4_zfill(st + 2 * Cfg::kTileBytes + 4 * kTileKeys + 4 * lane, dt, krow != kNoRow);
     }
   };
+  // the first tiles' positions, then their entries, then their copies: one
+  // latency each
+  KeyPage next;   // of the tile to be issued next
+  KeyPos npos;    // of the one after it
+  {
+    KeyPos p[STG + 1];
+    KeyPage e[STG];
 #pragma unroll
-  for (int s = 0; s < STG - 1; ++s) {
-    if (s < count) issue(s);
-    cp_commit();
+    for (int s = 0; s <= STG; ++s) p[s] = position();
+#pragma unroll
+    for (int s = 0; s < STG; ++s) e[s] = entry(p[s]);
+#pragma unroll
+    for (int s = 0; s < STG - 1; ++s) {
+      if (s < count) issue(e[s], s);
+      cp_commit();
+    }
+    next = e[STG - 1];
+    npos = p[STG];
   }
 
   // ---- the tiles
@@ -322,8 +343,10 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
     __syncwarp();   // every lane's copies of this stage have landed; the previous stage has been read
     {
       const int nslot = slot == 0 ? STG - 1 : slot - 1;
-      if (x + STG - 1 < count) issue(nslot);
+      if (x + STG - 1 < count) issue(next, nslot);
       cp_commit();
+      next = entry(npos);
+      npos = position();
     }
     const uint32_t st = ring_u + slot * Cfg::kStageBytes;
     float sa[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -433,7 +456,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
         }
         if (lane == 0) {
           s_kind[warp][cut] = cut ? kOpen : (row_end ? kEnds : kThrough);
-          s_cut[warp][cut] = RowCut{x0 + x - cur.t, cur.nt, cur.b, cur.g};
+          s_cut[warp][cut] = RowCut{x0 + static_cast<uint32_t>(x) - static_cast<uint32_t>(cur.t), cur.nt, cur.b, cur.g};
         }
       }
       fresh = true;
@@ -450,16 +473,16 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
   float* my_block = a.block_part + static_cast<size_t>(blockIdx.x) * 2 * psize;
   const int parts = (nrep * D + 127) / 128;
   int first = 0;   // the block's first warp with tiles
-  while (xb0 + (xb1 - xb0) * (first + 1) / kDpWarps == xb0) ++first;
+  while (warp_begin(first + 1) == xb0) ++first;
   const bool left = s_kind[first][0] != kNone;
   int shared = 0, open = -1;   // items so far; the chain that goes on past the block
   for (int w = 0; w <= kDpWarps; ++w) {
     if (w < kDpWarps ? s_kind[w][1] != kOpen : !left) continue;
     const int w0 = w < kDpWarps ? w : first;
     const RowCut cut = s_cut[w0][w < kDpWarps ? 1 : 0];
-    const long long end = min(cut.t0 + cut.nt, xb1);
-    const int w1 = static_cast<int>(((end - xb0) * kDpWarps - 1) / (xb1 - xb0));   // the warp of its last tile here
-    const bool right = cut.t0 + cut.nt > xb1;
+    const uint32_t end = min(cut.t0 + static_cast<uint32_t>(cut.nt), xb1);
+    const int w1 = static_cast<int>(((end - xb0) * kDpWarps - 1u) / nb);   // the warp of its last tile here
+    const bool right = cut.t0 + static_cast<uint32_t>(cut.nt) > xb1;
     if (right) open = w;
     for (int q = 0; q < parts; ++q, ++shared) {
       if (shared % kDpWarps != warp) continue;
@@ -491,18 +514,18 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
   // piece joins them
   const bool two = open >= 0 && open < kDpWarps;   // a row that goes on and began here (else it is the left one)
   if (!left && !two) return;
-  auto row_blocks = [&](int k, long long& b0, long long& b1) {
+  auto row_blocks = [&](int k, uint32_t& b0, uint32_t& b1) {
     const RowCut r = k == 0 ? s_cut[first][0] : s_cut[open][1];
-    b0 = (G * (r.t0 + 1) - 1) / U;
-    b1 = (G * (r.t0 + r.nt) - 1) / U;
+    b0 = axis.block_of(r.t0);
+    b1 = axis.block_of(r.t0 + static_cast<uint32_t>(r.nt) - 1u);
     return r;
   };
   __syncthreads();
   if (lane == 0 && warp < 2 && (warp == 0 ? left : two)) {
-    long long b0, b1;
+    uint32_t b0, b1;
     row_blocks(warp, b0, b1);
     __threadfence();
-    if (atomicAdd(a.tickets + b0, 1u) == static_cast<uint32_t>(b1 - b0)) {
+    if (atomicAdd(a.tickets + b0, 1u) == b1 - b0) {
       a.tickets[b0] = 0u;
       s_last[warp] = 1;
     }
@@ -511,7 +534,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
   __syncthreads();
   for (int k = 0; k < 2; ++k) {
     if (!s_last[k]) continue;
-    long long b0, b1;
+    uint32_t b0, b1;
     const RowCut r = row_blocks(k, b0, b1);
     for (int q = warp; q < parts; q += kDpWarps) {
       const int e = q * 128 + 4 * lane, h = e / D;

@@ -108,7 +108,7 @@ struct PagedLists {
 // Blocks that share a paged decode's work, at most (its scratch is sized for them).
 constexpr int kPagedMaxBlocks = 256;
 // Blocks of the prologue's backward, at most (a row of weight gradient shares each).
-constexpr int kPbMaxBlocks = 1024;
+constexpr int kPbMaxBlocks = 512;
 
 // Arguments of the append to a paged cache and of the prologue's backward, as the entry points take them.
 struct AppendPaged {

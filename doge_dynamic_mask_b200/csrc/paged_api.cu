@@ -65,6 +65,9 @@ dma_status_t check_paged_decode(int B, int max_pages, int page_size, int Hq, int
   const dma_status_t st = check_heads(Hq, Hkv, d);
   if (st != DMA_OK) return st;
   if (B > 65536 || static_cast<long long>(max_pages) * page_size > kMaxLen) return DMA_ERR_UNSUPPORTED;
+  // the attention counts 16-key tiles of all rows in 31 bits
+  const long long keys = std::min<long long>(visible_cap(max_pages, page_size, window, sinks), w);
+  if ((keys + 15) / 16 * B * Hkv >= 1LL << 31) return DMA_ERR_UNSUPPORTED;
   return DMA_OK;
 }
 

@@ -23,8 +23,8 @@
 // in flight need no registers or barriers.  A lane always holds the same
 // channels, so its share of dw accumulates in float32 registers over everything
 // the warp does; the shares are added in a fixed order (lane groups, warps,
-// blocks of a group, groups), so the result does not depend on timing; the last
-// block of a group, and the last group, add theirs, so there is no second launch.
+// blocks), so the result does not depend on timing; the last block to finish adds
+// the blocks' shares, so there is no second launch.
 #include <algorithm>
 
 #include "rope.cuh"
@@ -32,13 +32,11 @@
 namespace dma {
 namespace {
 
-constexpr int kPbThreads = 128;
+constexpr int kPbThreads = 256;
 constexpr int kPbWarps = kPbThreads / 32;
-constexpr int kPbMinBlocks = 4;
+constexpr int kPbMinBlocks = 2;
 constexpr int kPbStages = 4;                                     // ring steps per warp
-constexpr int kPbGroup = 24;                                     // blocks whose shares are added first
-constexpr int kPbTicketBytes = 256;                               // kPbMaxBlocks / kPbGroup + 2 tickets
-static_assert((kPbMaxBlocks / kPbGroup + 2) * 4 <= kPbTicketBytes, "a ticket per group and one for the groups");
+constexpr int kPbTicketBytes = 256;                              // one ticket
 constexpr int kPbSmemBytes = kPbWarps * kPbStages * 4 * 32 * 16;   // a step: four 16-byte chunks per lane
 
 struct PbArgs {
@@ -48,8 +46,8 @@ struct PbArgs {
   const int32_t* positions;
   uint16_t *dq, *dk;
   float *dq_w, *dk_w;
-  float* part;         // [blocks][2][d], then [groups of blocks][2][d]
-  uint32_t* tickets;   // [groups + 1], zero between calls: finished blocks of a group; finished groups
+  float* part;         // [blocks][2][d]: the blocks' shares
+  uint32_t* ticket;    // finished blocks, zero between calls
   float eps;
   int L;
   RowShare share;
@@ -62,7 +60,7 @@ __global__ void __launch_bounds__(kPbThreads, kPbMinBlocks)
   constexpr int H = D / 2;
   __shared__ __align__(16) float s_w[2][D];
   __shared__ __align__(16) double s_turn[H];
-  __shared__ float s_dw[kPbWarps][2][D];
+  __shared__ __align__(16) float s_dw[kPbWarps][2][D];
   pdl_wait();
   pdl_trigger();
   for (int c = threadIdx.x; c < D; c += kPbThreads) {
@@ -203,42 +201,43 @@ __global__ void __launch_bounds__(kPbThreads, kPbMinBlocks)
     for (int w = 0; w < kPbWarps; ++w) s += s_dw[w][c / D][c % D];
     a.part[static_cast<size_t>(blockIdx.x) * 2 * D + c] = s;
   }
-  // the last block of a group adds the group's shares, the last group all of them
-  const int blocks = static_cast<int>(gridDim.x), groups = (blocks + kPbGroup - 1) / kPbGroup;
-  const int group = static_cast<int>(blockIdx.x) / kPbGroup;
+  // the last block to finish adds the blocks' shares: four columns and every
+  // kRows-th block per thread, then the kRows sums
   __shared__ bool s_last;
-  auto last_of = [&](uint32_t* ticket, int n) {   // whether this block is the n-th to take the ticket
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      __threadfence();
-      s_last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(n - 1);
-      if (s_last) *ticket = 0u;
-      __threadfence();
-    }
-    __syncthreads();
-    return s_last;
-  };
-  auto add = [&](const float* rows, int n, int c) {
-    float s = 0.0f;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) s += __ldcg(rows + static_cast<size_t>(i) * 2 * D + c);
-    return s;
-  };
-  const int in_group = min(kPbGroup, blocks - group * kPbGroup);
-  float* sums = a.part + static_cast<size_t>(blocks) * 2 * D;
-  if (!last_of(a.tickets + group, in_group)) return;
-  for (int c = threadIdx.x; c < 2 * D; c += kPbThreads) {
-    const float s = add(a.part + static_cast<size_t>(group) * kPbGroup * 2 * D, in_group, c);
-    sums[static_cast<size_t>(group) * 2 * D + c] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1u;
+    if (s_last) *a.ticket = 0u;
+    __threadfence();
   }
-  if (!last_of(a.tickets + groups, groups)) return;
-  for (int c = threadIdx.x; c < 2 * D; c += kPbThreads) {
-    const float s = add(sums, groups, c);
-    if (c < D)
-      a.dq_w[c] = s;
-    else
-      a.dk_w[c - D] = s;
+  __syncthreads();
+  if (!s_last) return;
+  constexpr int kCols = 2 * D / 4, kRows = kPbThreads / kCols;
+  float4* sums = reinterpret_cast<float4*>(&s_dw[0][0][0]);   // [kRows][kCols]
+  const float4* part = reinterpret_cast<const float4*>(a.part);
+  const int col = threadIdx.x % kCols;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 16
+  for (int i = threadIdx.x / kCols; i < static_cast<int>(gridDim.x); i += kRows) {
+    const float4 x = __ldcg(part + static_cast<size_t>(i) * kCols + col);
+    v.x += x.x;
+    v.y += x.y;
+    v.z += x.z;
+    v.w += x.w;
   }
+  sums[threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.x >= kCols) return;
+#pragma unroll
+  for (int i = 1; i < kRows; ++i) {
+    const float4 x = sums[i * kCols + col];
+    v.x += x.x;
+    v.y += x.y;
+    v.z += x.z;
+    v.w += x.w;
+  }
+  *reinterpret_cast<float4*>((col < kCols / 2 ? a.dq_w : a.dk_w) + 4 * (col % (kCols / 2))) = v;
 }
 
 }  // namespace
@@ -263,14 +262,14 @@ cudaError_t launch_prologue_backward(const PrologueBackward& p, cudaStream_t s) 
   a.dk = static_cast<uint16_t*>(p.dk);
   a.dq_w = p.dq_norm_w;
   a.dk_w = p.dk_norm_w;
-  a.tickets = static_cast<uint32_t*>(p.scratch);
+  a.ticket = static_cast<uint32_t*>(p.scratch);
   a.part = reinterpret_cast<float*>(static_cast<char*>(p.scratch) + kPbTicketBytes);
   a.eps = p.eps;
   a.L = p.L;
   const int slots = std::min(kPbMinBlocks * nsm, kPbMaxBlocks);
   a.share = share_rows(p.B * p.L, p.Hq, p.Hkv, p.d, static_cast<long long>(slots) * kPbWarps);
-  // few items spread over blocks (and SMs) before they share one
-  const int blocks = std::min(a.share.items, slots);
+  // a warp per item: few blocks, and few shares to add, when there are few items
+  const int blocks = std::min((a.share.items + kPbWarps - 1) / kPbWarps, slots);
   auto* kernel = p.d == 64 ? prologue_bwd_kernel<64> : prologue_bwd_kernel<128>;
   const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), kPbSmemBytes);
   if (e != cudaSuccess) return e;
@@ -278,7 +277,7 @@ cudaError_t launch_prologue_backward(const PrologueBackward& p, cudaStream_t s) 
 }
 
 size_t prologue_backward_scratch_bytes(int d) {
-  return kPbTicketBytes + static_cast<size_t>(kPbMaxBlocks + kPbMaxBlocks / kPbGroup + 1) * 2 * d * sizeof(float);
+  return kPbTicketBytes + static_cast<size_t>(kPbMaxBlocks) * 2 * d * sizeof(float);
 }
 
 }  // namespace dma

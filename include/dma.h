@@ -383,7 +383,9 @@ DMA_API dma_status_t dma_prologue_backward(const void* q, const void* k, int64_t
  *   q, out        [B, Hq, d] bf16 (out written)
  *   lengths       [B] int32 in [0, max_pages * page_size]; 0 is an empty slot of a padded batch,
  *                 whose out row is zero.  Others are clamped and reported as DMA_ERR_BAD_LENGTH
- *   keep_window_size  any positive number; dt >= 0 as dma_append_paged writes it
+ *   keep_window_size  any positive number, with fewer than 2^35 kept keys in all if every
+ *                 sequence were as long as its table (B * Hkv rows of them); dt >= 0 as
+ *                 dma_append_paged writes it
  *   workspace     dma_decode_paged_workspace_size(...) bytes, zeroed once (status word first)
  * Keys in a page outside the pool are not seen (and reported).  Rows of a page past the
  * sequence's length are never used and may hold anything.  The same call gives the same bits.

@@ -81,6 +81,8 @@ def test_workspace_sizes(dma):
     assert f(64, 1024, 64, 16, 8, 128, 1 << 20) == f(1, 1, 1, 16, 8, 128, 1)
     assert f(4, 8, 16, 8, 3, 64, 128) == f(0, 8, 16, 8, 4, 64, 128) == f(4, 8, 16, 8, 4, 80, 128) == 0
     assert f(4, 1 << 20, 2, 8, 4, 64, 128) == 0            # more than 2^20 positions
+    assert f(2048, 1 << 16, 16, 16, 16, 64, 1 << 20) == 0  # 2^35 kept keys
+    assert f(2047, 1 << 16, 16, 16, 16, 64, 1 << 20) > 0
     assert dma.dma_prologue_backward_workspace_size(1, 1, 8, 4, 64) > 256
     assert dma.dma_prologue_backward_workspace_size(1, 1, 8, 3, 64) == 0
     assert dma.dma_status_string(8) == "DMA_ERR_BAD_PAGE"
