@@ -31,18 +31,21 @@
 namespace dma {
 namespace {
 
-constexpr int kDpWarps = 8;
-constexpr int kDpThreads = 32 * kDpWarps;
+constexpr int kDpMaxWarps = 16;
 constexpr int kTileKeys = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// d = 128 takes 204 registers a thread: eight warps, 25 KB of ring each.  d = 64
+// has room for sixteen, which get a short row's first tiles going sooner.
 template <int D>
 struct DpCfg {
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kWarps = D == 128 ? 8 : 16;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kStages = 3;
   static constexpr int kRowBytes = D * 2;
   static constexpr int kTileBytes = kTileKeys * kRowBytes;         // K rows (V rows follow)
   static constexpr int kStageBytes = 2 * kTileBytes + kTileKeys * 8;   // + the keys' masks (0 or -inf) and dt
-  static constexpr int kSmemBytes = kDpWarps * kStages * kStageBytes;
+  static constexpr int kSmemBytes = kWarps * kStages * kStageBytes;
 };
 
 struct DpArgs {
@@ -50,12 +53,20 @@ struct DpArgs {
   PagedLists lists;
   const uint16_t *q, *k, *v;
   uint16_t* out;
-  float* warp_part;   // [blocks][kDpWarps][2][Hq / Hkv][d + 2]: o, m, l of the pieces at a warp range's ends
-  float* block_part;  // [blocks][2][Hq / Hkv][d + 2]: the same for the blocks' ranges
+  float* warp_part;   // [blocks][warps][2][Hq / Hkv][piece_floats(d)]: o, m, l of the pieces at a warp range's ends
+  float* block_part;  // [blocks][2][Hq / Hkv][piece_floats(d)]: the same for the blocks' ranges
   uint32_t* tickets;  // [blocks], zero between calls: finished blocks of the row that begins in a block and leaves it
   float scale;
   int Hq;
 };
+
+// A head's piece: o[d], m, l, and zeros up to the next 32 bytes.  Written in whole
+// sectors: reading one back that was written in part would wait for memory.
+__host__ __device__ constexpr int piece_floats(int d) { return d + 8; }
+__device__ __forceinline__ void write_ml(float* dst, float m, float l) {
+  reinterpret_cast<float4*>(dst)[0] = make_float4(m, l, 0.0f, 0.0f);
+  reinterpret_cast<float4*>(dst)[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -137,25 +148,46 @@ struct Axis {
 };
 
 // Joins n pieces of a row for four channels of a head: piece(i) points at
-// piece i's o[d], m, l of that head; e is the first channel.
+// piece i's o[d], m, l of that head; e is the first channel.  Eight pieces at a
+// time, so a block's or a short row's pieces cost one or two latencies.
 template <int D, class F>
 __device__ __forceinline__ void join_pieces(int n, int e, F&& piece, float& M, float& den, float4& num) {
+  constexpr int kAtOnce = 8;
   M = -INFINITY;
   den = 0.0f;
   num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* p = piece(i);
-    const float2 lo = __ldcg(reinterpret_cast<const float2*>(p + e)), hi = __ldcg(reinterpret_cast<const float2*>(p + e + 2));
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + D));
-    const float N = fmaxf(M, ml.x);
-    const float f = M == N ? 1.0f : fast_exp2(M - N), w = ml.x == N ? (N == -INFINITY ? 0.0f : 1.0f) : fast_exp2(ml.x - N);
+  for (int i0 = 0; i0 < n; i0 += kAtOnce) {
+    float4 o[kAtOnce];
+    float2 ml[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      ml[i] = make_float2(-INFINITY, 0.0f);
+      if (i0 + i < n) {
+        const float* p = piece(i0 + i);
+        o[i] = __ldcg(reinterpret_cast<const float4*>(p + e));
+        ml[i] = __ldcg(reinterpret_cast<const float2*>(p + D));
+      }
+    }
+    float N = M;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) N = fmaxf(N, ml[i].x);
+    const float f = M == N ? 1.0f : fast_exp2(M - N);
     M = N;
-    den = fmaf(den, f, w * ml.y);
-    num.x = fmaf(num.x, f, w * lo.x);
-    num.y = fmaf(num.y, f, w * lo.y);
-    num.z = fmaf(num.z, f, w * hi.x);
-    num.w = fmaf(num.w, f, w * hi.y);
+    den *= f;
+    num.x *= f;
+    num.y *= f;
+    num.z *= f;
+    num.w *= f;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float w = ml[i].x == -INFINITY ? 0.0f : fast_exp2(ml[i].x - N);
+      den = fmaf(w, ml[i].y, den);
+      num.x = fmaf(w, o[i].x, num.x);
+      num.y = fmaf(w, o[i].y, num.y);
+      num.z = fmaf(w, o[i].z, num.z);
+      num.w = fmaf(w, o[i].w, num.w);
+    }
   }
 }
 
@@ -166,15 +198,14 @@ __device__ __forceinline__ void write_out(uint16_t* out, float den, const float4
 }
 
 template <int D>
-__global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __grid_constant__ DpArgs a) {
+__global__ void __launch_bounds__(DpCfg<D>::kThreads, 1) decode_paged_kernel(const __grid_constant__ DpArgs a) {
   using Cfg = DpCfg<D>;
+  constexpr int kDpWarps = Cfg::kWarps;
   constexpr int KS = D / 16;            // k16 steps of q.k; 16-channel tiles of o
   constexpr int CPR = D / 8;            // 16-byte chunks per row
   constexpr int RPI = 32 / CPR;         // rows per copy step of a warp
   constexpr int STG = Cfg::kStages;
   extern __shared__ __align__(128) unsigned char ring_all[];
-  __shared__ uint32_t s_pref[kDpThreads];      // tiles of the sequences up to and with this one
-  __shared__ uint32_t s_warp[kDpWarps];
   __shared__ RowCut s_cut[kDpWarps][2];
   __shared__ int s_kind[kDpWarps][2];
   __shared__ int s_last[2];
@@ -183,28 +214,27 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  // ---- the axis: U tiles; G blocks take at least a tile per warp
-  auto scan_step = [&](int b0, uint32_t before) {   // over sequences [b0, b0 + kDpThreads)
-    uint32_t x = b0 + tid < c.B ? static_cast<uint32_t>(seq_tiles(c, b0 + tid)) : 0u;
+  // ---- the axis: U tiles; G blocks take at least a tile per warp.  Every warp
+  // counts for itself, four sequences per lane at a time.
+  constexpr int kSeqs = 128;
+  uint32_t tiles[4], upto = 0;   // of this lane's sequences of a step; of the step up to and with them
+  auto count_step = [&](int b0) {   // returns the step's tiles
+    upto = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = b0 + 4 * lane + i;
+      tiles[i] = b < c.B ? static_cast<uint32_t>(seq_tiles(c, b)) : 0u;
+      upto += tiles[i];
+    }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
-      if (lane >= d) x += y;
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += y;
     }
-    __syncthreads();   // the last step's sums have been read
-    if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
-    uint32_t all = 0;
-#pragma unroll
-    for (int w = 0; w < kDpWarps; ++w) {
-      if (w < warp) x += s_warp[w];
-      all += s_warp[w];
-    }
-    s_pref[tid] = before + x;
-    return before + all;
+    return __shfl_sync(0xFFFFFFFFu, upto, 31);
   };
   uint32_t total = 0;
-  for (int b0 = 0; b0 < c.B; b0 += kDpThreads) total = scan_step(b0, total);
+  for (int b0 = 0; b0 < c.B; b0 += kSeqs) total += count_step(b0);
   const uint32_t U = total * static_cast<uint32_t>(c.Hkv);
   const uint32_t G = min(gridDim.x, (U + kDpWarps - 1u) / kDpWarps);
   if (blockIdx.x >= G) return;
@@ -217,26 +247,36 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
   {
     const uint32_t y = x0 >> (31 - __clz(c.Hkv));   // (Hkv is a power of two) tiles of sequences before x0's, rounded into it
     uint32_t before = 0;
-    for (int b0 = 0; b0 < c.B; b0 += kDpThreads) {
-      const uint32_t next = c.B > kDpThreads ? scan_step(b0, before) : total;
-      __syncthreads();
-      if (y >= before && y < next) {
-        int n = 0;   // sequences of this step that end at or before y
-#pragma unroll
-        for (int i = 0; i < kDpThreads; i += 32) n += __popc(__ballot_sync(0xFFFFFFFFu, s_pref[i + lane] <= y));
-        cur.b = b0 + n;
-        cur.enter(c);
-        const uint32_t rem = x0 - (n > 0 ? s_pref[n - 1] : before) * static_cast<uint32_t>(c.Hkv);
-        cur.g = static_cast<int>(rem / static_cast<uint32_t>(cur.nt));
-        cur.t = static_cast<int>(rem) - cur.g * cur.nt;
+    for (int b0 = 0; b0 < c.B; b0 += kSeqs) {
+      const uint32_t next = c.B > kSeqs ? before + count_step(b0) : total;
+      if (y >= next) {
+        before = next;
+        continue;
       }
-      before = next;
+      // the lane, then its sequence, whose tiles hold y
+      const int from = __popc(__ballot_sync(0xFFFFFFFFu, before + upto <= y));
+      cur.b = b0 + 4 * from;
+      before += __shfl_sync(0xFFFFFFFFu, upto - tiles[0] - tiles[1] - tiles[2] - tiles[3], from);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const uint32_t n = __shfl_sync(0xFFFFFFFFu, tiles[i], from);
+        if (cur.b == b0 + 4 * from + i && y >= before + n) {
+          before += n;
+          ++cur.b;
+        }
+      }
+      break;
     }
+    cur.enter(c);
+    const uint32_t rem = x0 - before * static_cast<uint32_t>(c.Hkv);
+    cur.g = static_cast<int>(rem / static_cast<uint32_t>(cur.nt));
+    cur.t = static_cast<int>(rem) - cur.g * cur.nt;
   }
   if (lane < 2) s_kind[warp][lane] = kNone;
   if (tid < 2) s_last[tid] = 0;
   const int nrep = a.Hq / c.Hkv;
-  const size_t psize = static_cast<size_t>(nrep) * (D + 2);
+  constexpr int PF = piece_floats(D);
+  const size_t psize = static_cast<size_t>(nrep) * PF;
   float* my_part = a.warp_part + (static_cast<size_t>(blockIdx.x) * kDpWarps + warp) * 2 * psize;
 
   // ---- the ring: position -> table entry -> copies of rows and dt, a tile apart
@@ -434,7 +474,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
       } else {
         // slot 0: the row began before this range; slot 1: it begins here and goes on
         const int cut = from_start ? 1 : 0;
-        float* dst = my_part + cut * psize + static_cast<size_t>(ha) * (D + 2);
+        float* dst = my_part + cut * psize + static_cast<size_t>(ha) * PF;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           if (ha < nrep) {
@@ -442,18 +482,12 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
             dst[16 * s + 8 + gid] = o[s][2];
           }
           if (hb < nrep) {
-            dst[D + 2 + 16 * s + gid] = o[s][1];
-            dst[D + 2 + 16 * s + 8 + gid] = o[s][3];
+            dst[PF + 16 * s + gid] = o[s][1];
+            dst[PF + 16 * s + 8 + gid] = o[s][3];
           }
         }
-        if (gid == 0 && ha < nrep) {
-          dst[D] = m0;
-          dst[D + 1] = L0;
-        }
-        if (gid == 0 && hb < nrep) {
-          dst[2 * D + 2] = m1;
-          dst[2 * D + 3] = L1;
-        }
+        if (gid == 0 && ha < nrep) write_ml(dst + D, m0, L0);
+        if (gid == 0 && hb < nrep) write_ml(dst + PF + D, m1, L1);
         if (lane == 0) {
           s_kind[warp][cut] = cut ? kOpen : (row_end ? kEnds : kThrough);
           s_cut[warp][cut] = RowCut{x0 + static_cast<uint32_t>(x) - static_cast<uint32_t>(cur.t), cur.nt, cur.b, cur.g};
@@ -468,54 +502,63 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
 
   // ---- the block's pieces, row by row.  Chain w < kDpWarps: the row that begins
   // in warp w and leaves its range; chain kDpWarps: the row that began before the
-  // block.  The warps share out (chain, 128 channels of its heads).
+  // block.  Lane w finds chain w; the warps share out (chain, 128 channels of its
+  // heads).
   const float* warp_part = a.warp_part + static_cast<size_t>(blockIdx.x) * kDpWarps * 2 * psize;
   float* my_block = a.block_part + static_cast<size_t>(blockIdx.x) * 2 * psize;
   const int parts = (nrep * D + 127) / 128;
-  int first = 0;   // the block's first warp with tiles
-  while (warp_begin(first + 1) == xb0) ++first;
-  const bool left = s_kind[first][0] != kNone;
-  int shared = 0, open = -1;   // items so far; the chain that goes on past the block
-  for (int w = 0; w <= kDpWarps; ++w) {
-    if (w < kDpWarps ? s_kind[w][1] != kOpen : !left) continue;
-    const int w0 = w < kDpWarps ? w : first;
-    const RowCut cut = s_cut[w0][w < kDpWarps ? 1 : 0];
+  const uint32_t busy = __ballot_sync(0xFFFFFFFFu, lane < kDpWarps && warp_begin(lane + 1) != warp_begin(lane));   // warps with tiles
+  const int first = __ffs(static_cast<int>(busy)) - 1;
+  RowCut cut{};
+  int w0 = 0, w1 = 0;      // the chain's warps
+  bool right = false;      // it goes on past the block
+  const bool mine = lane < kDpWarps ? s_kind[lane][1] == kOpen : lane == kDpWarps && s_kind[first][0] != kNone;
+  if (mine) {
+    w0 = lane < kDpWarps ? lane : first;
+    cut = s_cut[w0][lane < kDpWarps ? 1 : 0];
     const uint32_t end = min(cut.t0 + static_cast<uint32_t>(cut.nt), xb1);
-    const int w1 = static_cast<int>(((end - xb0) * kDpWarps - 1u) / nb);   // the warp of its last tile here
-    const bool right = cut.t0 + static_cast<uint32_t>(cut.nt) > xb1;
-    if (right) open = w;
-    for (int q = 0; q < parts; ++q, ++shared) {
-      if (shared % kDpWarps != warp) continue;
-      const int e = q * 128 + 4 * lane, h = e / D;
-      if (h >= nrep) continue;
-      int n = 0;
-      uint32_t order = 0;   // the chain's warps that have tiles, four bits each
-      for (int i = w0; i <= w1; ++i)
-        if (s_kind[i][0] != kNone || i == w0) order |= static_cast<uint32_t>(i) << (4 * n++);
-      const float* base = warp_part + static_cast<size_t>(h) * (D + 2);
-      float M, den;
-      float4 num;
-      join_pieces<D>(
-          n, e % D,
-          [&](int i) { return base + (2 * (order >> (4 * i) & 15u) + (i == 0 && w < kDpWarps ? 1 : 0)) * psize; }, M, den,
-          num);
-      if (w < kDpWarps && !right) {
-        write_out(a.out + (static_cast<size_t>(cut.b) * a.Hq + cut.g * nrep + h) * D + e % D, den, num);
-      } else {
-        float* dst = my_block + (w < kDpWarps ? psize : 0) + static_cast<size_t>(h) * (D + 2);
-        *reinterpret_cast<float2*>(dst + e % D) = make_float2(num.x, num.y);
-        *reinterpret_cast<float2*>(dst + e % D + 2) = make_float2(num.z, num.w);
-        if (e % D == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(M, den);
-      }
+    w1 = static_cast<int>(((end - xb0) * kDpWarps - 1u) / nb);   // the warp of its last tile here
+    right = cut.t0 + static_cast<uint32_t>(cut.nt) > xb1;
+  }
+  const uint32_t chains = __ballot_sync(0xFFFFFFFFu, mine), opens = __ballot_sync(0xFFFFFFFFu, right);
+  const bool left = chains >> kDpWarps & 1u;
+  for (int it = warp; it < __popc(chains) * parts; it += kDpWarps) {
+    uint32_t rest = chains;
+    for (int i = it / parts; i > 0; --i) rest &= rest - 1u;
+    const int w = __ffs(static_cast<int>(rest)) - 1;
+    const int c0 = __shfl_sync(0xFFFFFFFFu, w0, w), c1 = __shfl_sync(0xFFFFFFFFu, w1, w);
+    const int cb = __shfl_sync(0xFFFFFFFFu, cut.b, w), cg = __shfl_sync(0xFFFFFFFFu, cut.g, w);
+    const int e = it % parts * 128 + 4 * lane, h = e / D;
+    if (h >= nrep) continue;
+    uint32_t todo = busy & (0xFFFFFFFFu << c0) & (0xFFFFFFFFu >> (31 - c1));   // its warps that have tiles
+    const int n = __popc(todo);
+    const float* base = warp_part + static_cast<size_t>(h) * PF;
+    float M, den;
+    float4 num;
+    join_pieces<D>(
+        n, e % D,
+        [&](int i) {
+          const int from = __ffs(static_cast<int>(todo)) - 1;
+          todo &= todo - 1u;
+          return base + (2 * from + (i == 0 && w < kDpWarps ? 1 : 0)) * psize;
+        },
+        M, den, num);
+    if (w < kDpWarps && !(opens >> w & 1u)) {
+      write_out(a.out + (static_cast<size_t>(cb) * a.Hq + cg * nrep + h) * D + e % D, den, num);
+    } else {
+      float* dst = my_block + (w < kDpWarps ? psize : 0) + static_cast<size_t>(h) * PF;
+      *reinterpret_cast<float4*>(dst + e % D) = num;
+      if (e % D == 0) write_ml(dst + D, M, den);
     }
   }
 
   // ---- rows shared with other blocks: the one that finishes such a row's last
   // piece joins them
-  const bool two = open >= 0 && open < kDpWarps;   // a row that goes on and began here (else it is the left one)
+  const uint32_t here = opens & ((1u << kDpWarps) - 1u);   // a row that goes on and began here (else it is the left one)
+  const bool two = here != 0u;
   if (!left && !two) return;
   auto row_blocks = [&](int k, uint32_t& b0, uint32_t& b1) {
-    const RowCut r = k == 0 ? s_cut[first][0] : s_cut[open][1];
+    const RowCut r = k == 0 ? s_cut[first][0] : s_cut[__ffs(static_cast<int>(here)) - 1][1];
     b0 = axis.block_of(r.t0);
     b1 = axis.block_of(r.t0 + static_cast<uint32_t>(r.nt) - 1u);
     return r;
@@ -524,12 +567,13 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
   if (lane == 0 && warp < 2 && (warp == 0 ? left : two)) {
     uint32_t b0, b1;
     row_blocks(warp, b0, b1);
-    __threadfence();
-    if (atomicAdd(a.tickets + b0, 1u) == b1 - b0) {
+    // releases this block's pieces (written before the barrier) and acquires the others'
+    uint32_t before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.tickets + b0) : "memory");
+    if (before == b1 - b0) {
       a.tickets[b0] = 0u;
       s_last[warp] = 1;
     }
-    __threadfence();
   }
   __syncthreads();
   for (int k = 0; k < 2; ++k) {
@@ -539,7 +583,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) decode_paged_kernel(const __gri
     for (int q = warp; q < parts; q += kDpWarps) {
       const int e = q * 128 + 4 * lane, h = e / D;
       if (h >= nrep) continue;
-      const float* base = a.block_part + static_cast<size_t>(b0) * 2 * psize + static_cast<size_t>(h) * (D + 2);
+      const float* base = a.block_part + static_cast<size_t>(b0) * 2 * psize + static_cast<size_t>(h) * PF;
       float M, den;
       float4 num;
       join_pieces<D>(
@@ -553,7 +597,7 @@ template <int D>
 cudaError_t launch_dp(const DpArgs& a, int blocks, cudaStream_t s) {
   const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(decode_paged_kernel<D>), DpCfg<D>::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_after(decode_paged_kernel<D>, dim3(blocks), dim3(kDpThreads), DpCfg<D>::kSmemBytes, s, a);
+  return launch_after(decode_paged_kernel<D>, dim3(blocks), dim3(DpCfg<D>::kThreads), DpCfg<D>::kSmemBytes, s, a);
 }
 
 }  // namespace
@@ -562,7 +606,7 @@ cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, cons
                               const void* v_pages, int Hq, float scale, void* scratch, void* out, cudaStream_t s) {
   const int nsm = sm_count();
   if (nsm <= 0) return cudaErrorInvalidDevice;
-  const size_t psize = static_cast<size_t>(Hq / c.Hkv) * (c.d + 2);
+  const size_t psize = static_cast<size_t>(Hq / c.Hkv) * piece_floats(c.d);
   DpArgs a;
   a.c = c;
   a.lists = lists;
@@ -581,7 +625,7 @@ cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, cons
 
 size_t attn_paged_scratch_bytes(int Hq, int Hkv, int d) {
   return kPagedMaxBlocks * 4 +
-         static_cast<size_t>(kPagedMaxBlocks) * (1 + kDpWarps) * 2 * (Hq / Hkv) * (d + 2) * sizeof(float);
+         static_cast<size_t>(kPagedMaxBlocks) * (1 + kDpMaxWarps) * 2 * (Hq / Hkv) * piece_floats(d) * sizeof(float);
 }
 
 }  // namespace dma
