@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(DpCfg<D>::kThreads, 1) decode_paged_kernel(con
       mma16816(o[s], va, ph0, ph1);
       mma16816(o[s], va, pe0, pe1);
     }
+    const int used = slot;
     slot = slot + 1 == STG ? 0 : slot + 1;
 
     const bool row_end = cur.t + 1 == cur.nt;
@@ -456,44 +457,44 @@ __global__ void __launch_bounds__(DpCfg<D>::kThreads, 1) decode_paged_kernel(con
         L1 += __shfl_xor_sync(0xFFFFFFFFu, L1, d);
       }
       const int ha = 2 * t4, hb = ha + 1;
-      if (row_end && from_start) {
-        const float i0 = L0 == 0.0f ? 0.0f : 1.0f / L0, i1 = L1 == 0.0f ? 0.0f : 1.0f / L1;
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) +
-                             (static_cast<size_t>(cur.b) * a.Hq + cur.g * nrep + ha) * D + gid;
+      // through the stage just read (its K rows' place), so that rows of o leave in
+      // whole 128-byte lines: written from the accumulators as they lie, four bytes a
+      // lane, a block's pieces took 1 to 2 us
+      float* turn = reinterpret_cast<float*>(ring + used * Cfg::kStageBytes);   // [head][d]
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          if (ha < nrep) {
-            dst[16 * s] = __float2bfloat16_rn(o[s][0] * i0);
-            dst[16 * s + 8] = __float2bfloat16_rn(o[s][2] * i0);
-          }
-          if (hb < nrep) {
-            dst[D + 16 * s] = __float2bfloat16_rn(o[s][1] * i1);
-            dst[D + 16 * s + 8] = __float2bfloat16_rn(o[s][3] * i1);
-          }
+      for (int s = 0; s < KS; ++s) {
+        if (ha < nrep) {
+          turn[ha * D + 16 * s + gid] = o[s][0];
+          turn[ha * D + 16 * s + 8 + gid] = o[s][2];
+        }
+        if (hb < nrep) {
+          turn[hb * D + 16 * s + gid] = o[s][1];
+          turn[hb * D + 16 * s + 8 + gid] = o[s][3];
+        }
+      }
+      __syncwarp();
+      if (row_end && from_start) {
+        uint16_t* dst = a.out + (static_cast<size_t>(cur.b) * a.Hq + cur.g * nrep) * D;
+        for (int e = 4 * lane; e < (nrep * D + 127) / 128 * 128; e += 128) {   // the whole warp shuffles
+          const int h = e / D;
+          const float la = __shfl_sync(0xFFFFFFFFu, L0, h >> 1 & 3), lb = __shfl_sync(0xFFFFFFFFu, L1, h >> 1 & 3);
+          if (h < nrep) write_out(dst + e, h & 1 ? lb : la, *reinterpret_cast<const float4*>(turn + e));
         }
       } else {
         // slot 0: the row began before this range; slot 1: it begins here and goes on
         const int cut = from_start ? 1 : 0;
-        float* dst = my_part + cut * psize + static_cast<size_t>(ha) * PF;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          if (ha < nrep) {
-            dst[16 * s + gid] = o[s][0];
-            dst[16 * s + 8 + gid] = o[s][2];
-          }
-          if (hb < nrep) {
-            dst[PF + 16 * s + gid] = o[s][1];
-            dst[PF + 16 * s + 8 + gid] = o[s][3];
-          }
-        }
-        if (gid == 0 && ha < nrep) write_ml(dst + D, m0, L0);
-        if (gid == 0 && hb < nrep) write_ml(dst + PF + D, m1, L1);
+        float* dst = my_part + cut * psize;
+        for (int e = 4 * lane; e < nrep * D; e += 128)
+          *reinterpret_cast<float4*>(dst + e / D * PF + e % D) = *reinterpret_cast<const float4*>(turn + e);
+        if (gid == 0 && ha < nrep) write_ml(dst + ha * PF + D, m0, L0);
+        if (gid == 0 && hb < nrep) write_ml(dst + hb * PF + D, m1, L1);
         if (lane == 0) {
           s_kind[warp][cut] = cut ? kOpen : (row_end ? kEnds : kThrough);
           s_cut[warp][cut] = RowCut{x0 + static_cast<uint32_t>(x) - static_cast<uint32_t>(cur.t), cur.nt, cur.b, cur.g};
         }
       }
       fresh = true;
+      __syncwarp();   // the stage is free again
     }
     cur.next(c);
   }
