@@ -5,21 +5,27 @@
 // (prepare_dynamic_mask: of the keys a query sees, the keep_window_size best by
 // dt; ties go to the lower index).  dt of every cached token lies in its page.
 //
-// Design.  One cluster of CTAs per (sequence, kv head).  The row is read once:
-// a sample (2048 keys, of long rows 4096, in runs of eight spread over the row)
-// gives a threshold that the w-th best key is above with four standard
+// Design.  One CTA, or a cluster of them, per (sequence, kv head).  The row is
+// read once: a sample (2048 keys, of long rows 4096, in runs of eight spread over
+// the row) gives a threshold that the w-th best key is above with four standard
 // deviations to spare, and every thread appends the keys at or above it that it
-// meets (about 1.6 w in all at 64k keys) to a list of its own in shared memory:
-// the pass is bound by integer instructions, and a list per warp, whose places
-// come from votes and population counts, took four times as many per key.  A
-// histogram of the collected keys over the cluster finds the w-th key's bin;
-// keys above the bin are kept, and the few inside are ranked one against
-// another by (dt, index).  The bound is the one read of dt plus the latency of
-// those steps; a row is spread over up to eight CTAs when there are fewer rows
-// than SMs.  Rows the sample misjudges (more ties at the threshold than the
-// lists hold, too few keys) are selected exactly by the cluster's first CTA in a
-// few more passes.  The order of the list is fixed by the row alone, so the
-// attention adds its terms in the same order every time.
+// meets (about 1.6 w in all at 64k keys) to a list of its own in shared memory,
+// by predicated instructions without votes or branches; the few keys that find
+// their list full spill to a list of the CTA.  A histogram of the collected keys
+// over the cluster finds the w-th key's bin; keys above the bin are kept, and the
+// few inside are ranked one against another by (dt, index).  When one value takes
+// many places of the sample around the threshold (a model at its start has dt = 1
+// everywhere) only the keys above it are collected, and the lowest-indexed ones
+// of that value fill the list.  Rows the sample misjudges (too few keys, too many
+// in one bin) are selected exactly by the cluster's first CTA in a few more
+// passes.  The order of the list is fixed by the row alone, so the attention adds
+// its terms in the same order every time.
+//
+// What bounds it: integer instructions and the latency of its steps, not the one
+// read of dt.  512 rows of 32k to 64k keys, w = 2048: about 50 us for 100 MB (16 us
+// at the copy rate); in cycles of a CTA of 512 threads: sample 6k, threshold 3k,
+// collection 27k, bins 6k, writing 7k.  Lists per warp built with votes at 256
+// threads took 77k cycles a CTA, four CTAs an SM instead of two: the same time.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -54,6 +60,7 @@ struct SpShared {
   uint32_t bin[3];                       // top_bin's answer
   uint32_t keys, sure, spills;           // this CTA's collected keys, those above the bin, those in `spill`
   uint32_t edges, exact;                 // (first CTA) keys in `edge`; the row needs the exact selection
+  uint32_t ties;                         // this CTA's keys of the tied value
 };
 // dynamic shared memory: SpShared, then the collected keys' dt bits and
 // positions, [room + kSlack][2][THREADS] (first the sample's values)
@@ -118,7 +125,7 @@ __device__ __forceinline__ uint32_t load_oct(const PagedCache& c, const Row& r, 
   uint32_t seen = oct_mask(r, x, j0);
   int off;
   int slot = page_slot(c, j0, off);
-  if (VEC) {
+  if constexpr (VEC) {
     page = checked_page(c, page);
     if (page < 0) return 0u;
     const uint4* src = reinterpret_cast<const uint4*>(c.dt_pages + dt_offset(c, page, off, r.g));
@@ -131,27 +138,24 @@ __device__ __forceinline__ uint32_t load_oct(const PagedCache& c, const Row& r, 
     v[5] = b.y;
     v[6] = b.z;
     v[7] = b.w;
-    return seen;
-  }
-  bool fresh = true;   // the page at hand has not been checked
+  } else {
+    // the entries of all eight first, then their dt: one latency each
+    int pages[8], offs[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    v[e] = 0u;
-    if (off == c.page_size) {
-      off = 0;
-      ++slot;
-      if (seen >> e) page = __ldg(r.table + slot);
-      fresh = true;
+    for (int e = 0; e < 8; ++e) {
+      pages[e] = e == 0 ? page : pages[e > 0 ? e - 1 : 0];
+      if (off == c.page_size) {
+        off = 0;
+        ++slot;
+        if (seen >> e) pages[e] = __ldg(r.table + slot);
+      }
+      offs[e] = off++;
     }
-    if (seen >> e & 1u) {
-      if (fresh) page = checked_page(c, page);
-      fresh = false;
-      if (page < 0)
-        seen &= ~(1u << e);
-      else
-        v[e] = __float_as_uint(__ldg(c.dt_pages + dt_offset(c, page, off, r.g)));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if ((seen >> e & 1u) && checked_page(c, pages[e]) < 0) seen &= ~(1u << e);
+      v[e] = seen >> e & 1u ? __float_as_uint(__ldg(c.dt_pages + dt_offset(c, pages[e], offs[e], r.g))) : 0u;
     }
-    ++off;
   }
   return seen;
 }
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
   uint32_t* sample = list;
   const int socts = min(view.n > kSpSampleLong ? kSpSample : kSpSample / 2, r.no);
   for (int i = tid; i < kBins; i += THREADS) sm.hist[i] = 0;
-  if (tid == 0) sm.keys = sm.sure = sm.spills = sm.edges = sm.exact = 0u;
+  if (tid == 0) sm.keys = sm.sure = sm.spills = sm.edges = sm.exact = sm.ties = 0u;
   uint32_t ns = 0, thr = 0xFFFFFFFFu, smax = 0u;
   static_assert(THREADS >= kSpSample, "a sampled oct per thread, and the sample fits eight list rows");
   if (tid < socts) {
@@ -410,6 +414,7 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
   block_range<THREADS>(sm, ns, thr, smax);
   uint32_t k = static_cast<uint32_t>(
       sample_rank(static_cast<float>(w) * static_cast<float>(ns) / static_cast<float>(view.n)));
+  bool tied = thr == smax;   // the threshold is one value with many keys of the sample
   if (k < ns) {
     uint32_t lo = thr, hi = smax;
     while (lo < hi) {
@@ -428,25 +433,30 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
       hi = min(hi, l2 + ((1u << s) - 1u));
       lo = l2;
       if (cnt <= 16u) break;   // its lower edge takes a few more keys than the exact value would
+      tied = lo == hi;
     }
     thr = lo;
   }
+  const uint32_t tie = thr;
+  if (tied || thr == 0u) {   // (0: positions that are not seen read as 0, below every threshold)
+    tied = true;
+    ++thr;
+  }
   __syncthreads();   // the sample has been read: keys are written over it
 
-  // ---- collect, an oct per thread and step.  Positions that are not seen read
-  // as 0, below any threshold; a threshold of 0 (dt that underflowed among the w
-  // best) is left to the exact selection.
+  // ---- collect, an oct per thread and step
   const int shift = bin_shift(smax > thr ? smax - thr : 0u);
   auto bin_of = [&](uint32_t bits) { return min(static_cast<uint32_t>(kBins - 1), (bits - thr) >> shift); };
   constexpr uint32_t kStep = 8u * THREADS;   // bytes between a thread's keys
   const uint32_t first = smem_u32(list + tid);
   const uint32_t full = first + static_cast<uint32_t>(room) * kStep;
   uint32_t at = first;   // place of this thread's next key
-  if (thr > 0u) {
-    // each warp of the cluster takes a contiguous part of the row, 32 octs at a
-    // time, so that the list ends up roughly in the order of the positions
-    const int part = (r.no + csize * THREADS - 1) / (csize * THREADS) * 32;
-    const int xw = min(r.no, (rank * (THREADS / 32) + warp) * part), xe = min(r.no, xw + part);
+  uint32_t n_tied = 0;
+  // each warp of the cluster takes a contiguous part of the row, 32 octs at a
+  // time, so that the list ends up roughly in the order of the positions
+  const int part = (r.no + csize * THREADS - 1) / (csize * THREADS) * 32;
+  const int xw = min(r.no, (rank * (THREADS / 32) + warp) * part), xe = min(r.no, xw + part);
+  {
     int page[Cfg::kUnroll];
 #pragma unroll
     for (int u = 0; u < Cfg::kUnroll; ++u) page[u] = oct_page(c, r, xw + lane + 32 * u, xe);
@@ -461,6 +471,10 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
         if (seen[u] != 255u) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[u][e] = seen[u] >> e & 1u ? v[u][e] : 0u;
+        }
+        if (tied) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) n_tied += (seen[u] >> e & 1u) && v[u][e] == tie;
         }
         const uint32_t j0 = static_cast<uint32_t>(oct_position(r, x + 32 * u));
 #pragma unroll
@@ -484,22 +498,31 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
   auto key_pos = [&](int i) { return static_cast<int>(list[(2 * i + 1) * THREADS + tid]); };
   {
     const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(n));
-    if (lane == 0) atomicAdd(&sm.keys, all);
+    n_tied = __reduce_add_sync(0xFFFFFFFFu, n_tied);
+    if (lane == 0) {
+      atomicAdd(&sm.keys, all);
+      atomicAdd(&sm.ties, n_tied);
+      sm.warp[2][warp] = n_tied;
+    }
     for (int i = 0; i < n; ++i) atomicAdd(&sm.hist[bin_of(key_bits(i))], 1u);
   }
 
   // ---- the w-th key's bin, over the cluster
   sync_all();
-  uint32_t wbin, need, bad = 0, total = 0;
+  uint32_t bad = 0, total = 0, ties = 0, ties_before = 0;   // ..before: in the CTAs before this one
   for (int q = 0; q < csize; ++q) {
     const SpShared* other = of_rank(q);
     bad |= other->spills > static_cast<uint32_t>(kSpSpill);
     total += other->keys;
+    ties += other->ties;
+    if (q < rank) ties_before += other->ties;
   }
-  bad |= total < static_cast<uint32_t>(w) || thr == 0u;
+  // keys of the tied value that the list still has room for
+  const uint32_t fill = total < static_cast<uint32_t>(w) ? static_cast<uint32_t>(w) - total : 0u;
+  bad |= fill > ties;
   SpShared* lead = of_rank(0);
-  if (!bad && rank == 0) {
-    uint32_t cnt;
+  if (!bad && fill == 0u && rank == 0) {
+    uint32_t wbin, need, cnt;
     top_bin<THREADS>(
         sm, static_cast<uint32_t>(w),
         [&](int i) {
@@ -515,21 +538,22 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
     if (tid == 0 && cnt > static_cast<uint32_t>(kSpEdge)) sm.exact = 1u;
   }
   sync_all();
-  wbin = lead->bin[0];
-  need = lead->bin[1];
+  const int wbin = fill > 0u ? -1 : static_cast<int>(lead->bin[0]);   // below all bins: every collected key is kept
+  const uint32_t need = fill > 0u ? 0u : lead->bin[1];
   bad |= lead->exact;
   uint32_t before = 0;   // the warp's sure keys before this thread's
   if (!bad) {
     // keys inside the bin go to the first CTA (they are ranked by value, so
     // their order there does not matter); keys above it are counted
     for (int i = 0; i < n; ++i) {
-      const uint32_t bits = key_bits(i), bin = bin_of(bits);
+      const uint32_t bits = key_bits(i);
+      const int bin = static_cast<int>(bin_of(bits));
       before += bin > wbin;
       if (bin == wbin) lead->edge[atomicAdd(&lead->edges, 1u)] = composite_key(bits, key_pos(i));
     }
     if (tid < sm.spills) {
       const uint64_t key = sm.spill[tid];
-      const uint32_t bin = bin_of(static_cast<uint32_t>(key >> 32));
+      const int bin = static_cast<int>(bin_of(static_cast<uint32_t>(key >> 32)));
       if (bin > wbin) atomicAdd(&sm.sure, 1u);
       if (bin == wbin) lead->edge[atomicAdd(&lead->edges, 1u)] = key;
     }
@@ -552,12 +576,12 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
     uint32_t pos = start + warps_before(sm.warp[1]) + before;
     for (int i = 0; i < n; ++i) {
       const uint32_t bits = key_bits(i);
-      if (bin_of(bits) > wbin) out.put(pos++, static_cast<int>(key_pos(i)), bits);
+      if (static_cast<int>(bin_of(bits)) > wbin) out.put(pos++, static_cast<int>(key_pos(i)), bits);
     }
     // then the spilled ones, in the order of their positions
     const uint32_t spills = sm.spills;
     const uint64_t key = tid < spills ? sm.spill[tid] : 0ull;
-    auto is_sure = [&](uint64_t k) { return bin_of(static_cast<uint32_t>(k >> 32)) > wbin; };
+    auto is_sure = [&](uint64_t k) { return static_cast<int>(bin_of(static_cast<uint32_t>(k >> 32))) > wbin; };
     if (spills > 0) {
       pos = start + __reduce_add_sync(0xFFFFFFFFu, lane < THREADS / 32 ? sm.warp[1][lane] : 0u);
       if (tid < spills && is_sure(key)) {
@@ -565,6 +589,27 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
           pos += is_sure(sm.spill[i]) && composite_index(sm.spill[i]) < composite_index(key);
         out.put(pos, key);
       }
+    }
+    // the lowest-indexed keys of the tied value: a warp whose part has some of them
+    // reads it again
+    uint32_t trank = ties_before + warps_before(sm.warp[2]);
+    for (int x0 = xw; x0 < xe && trank < fill; x0 += 32) {
+      const int x = x0 + lane;
+      uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      const uint32_t seen = load_oct<VEC>(c, r, x, oct_page(c, r, x, xe), v, xe);
+      uint32_t m = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m |= (seen >> e & 1u) && v[e] == tie ? 1u << e : 0u;
+      uint32_t upto = __popc(m);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += y;
+      }
+      uint32_t mine = trank + upto - __popc(m);
+      for (; m && mine < fill; m &= m - 1u, ++mine)
+        out.put(total + mine, oct_position(r, x) + __ffs(static_cast<int>(m)) - 1, tie);
+      trank += __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
     if (rank == 0) {
       // the bin's `need` best keys, each at its rank
@@ -581,21 +626,35 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
   if (bad && rank == 0) select_exact<THREADS, VEC>(c, out, r, w, sm);
 }
 
-template <int THREADS, bool VEC, bool CLUSTER>
-cudaError_t launch_sp(const PagedCache& c, const PagedLists& lists, int rows, int csize, cudaStream_t s) {
-  // list entries per thread in the longest row the table can hold: its share of
-  // the keys expected above the threshold, and four standard deviations (of the
-  // threshold's rank in the sample, and of the share; the few keys beyond spill);
-  // windows larger than shared memory holds are selected exactly
+// List entries per thread in the longest row the table can hold, over `threads`
+// threads: the share of the keys expected above the threshold, and its standard
+// deviation (of the threshold's rank in the sample, and of the share).
+struct Share {
+  double mean, deviation;
+};
+
+Share share_of(const PagedCache& c, int threads) {
   const double keys = static_cast<double>(c.max_pages) * c.page_size;
   const double ratio = keys / (keys > kSpSampleLong ? 8.0 * kSpSample : 4.0 * kSpSample);   // keys per sampled one
   const double rank = sample_rank(c.w / ratio);
-  const double share = rank * ratio / (static_cast<double>(THREADS) * csize);
-  constexpr int kSlack = SpCfg<THREADS>::kSlack;
-  const int most = (226 * 1024 - static_cast<int>(sizeof(SpShared))) / (8 * THREADS) - kSlack;
-  const int room = std::max(8, static_cast<int>(std::min(share + 4.0 * std::sqrt(share + share * share / rank) + 2.0,
-                                                         static_cast<double>(most))));
-  const int smem = static_cast<int>(sizeof(SpShared)) + 8 * (room + kSlack) * THREADS;
+  const double mean = rank * ratio / threads;
+  return Share{mean, std::sqrt(mean + mean * mean / rank)};
+}
+
+// list entries per thread that let `per_sm` CTAs share an SM's shared memory
+template <int THREADS>
+int most_room(int per_sm) {
+  return ((227 * 1024) / per_sm - 1024 - static_cast<int>(sizeof(SpShared))) / (8 * THREADS) - SpCfg<THREADS>::kSlack;
+}
+
+template <int THREADS, bool VEC, bool CLUSTER>
+cudaError_t launch_sp(const PagedCache& c, const PagedLists& lists, int rows, int csize, cudaStream_t s) {
+  // four standard deviations of room where shared memory has it (a few keys
+  // spill where it has less; windows far beyond it are selected exactly)
+  const Share share = share_of(c, THREADS * csize);
+  const int room = std::max(8, static_cast<int>(std::min(share.mean + 4.0 * share.deviation + 2.0,
+                                                         static_cast<double>(most_room<THREADS>(SpCfg<THREADS>::kMinBlocks)))));
+  const int smem = static_cast<int>(sizeof(SpShared)) + 8 * (room + SpCfg<THREADS>::kSlack) * THREADS;
   const void* fn = reinterpret_cast<const void*>(select_paged_kernel<THREADS, VEC, CLUSTER>);
   const cudaError_t e = ensure_dyn_smem(fn, smem);
   if (e != cudaSuccess) return e;
@@ -622,15 +681,26 @@ cudaError_t launch_select_paged(const PagedCache& c, const PagedLists& lists, cu
   const int nsm = sm_count();
   if (nsm <= 0) return cudaErrorInvalidDevice;
   const int rows = c.B * c.Hkv;
-  // CTAs per row: as many as the SMs hold at once, each with 4096 keys or more
-  // of the longest row the table can hold
+  const bool vec = c.page_size % 8 == 0;
+  // few rows: as many CTAs per row as the SMs hold at once, each with 4096 keys or
+  // more of the longest row the table can hold (one row of 500k keys: 18 us on
+  // eight CTAs)
   const long long keys = static_cast<long long>(c.max_pages) * c.page_size;
   int csize = 1;
   while (csize < 8 && 2LL * csize * rows <= nsm && keys >= 4096LL * 2 * csize) csize *= 2;
-  const bool vec = c.page_size % 8 == 0;
   if (csize > 1)
     return vec ? launch_sp<1024, true, true>(c, lists, rows, csize, s)
                : launch_sp<1024, false, true>(c, lists, rows, csize, s);
+  // many rows: one CTA each, or as many as give the lists of a large window room
+  // while two CTAs share an SM (512 rows of 32k to 64k keys at w = 4000, the step with
+  // its attention: 306 us with one CTA an SM, 258 us so)
+  for (; csize < 8; csize *= 2) {
+    const Share share = share_of(c, 512 * csize);
+    if (share.mean + 2.0 * share.deviation <= most_room<512>(2)) break;
+  }
+  if (csize > 1)
+    return vec ? launch_sp<512, true, true>(c, lists, rows, csize, s)
+               : launch_sp<512, false, true>(c, lists, rows, csize, s);
   return vec ? launch_sp<512, true, false>(c, lists, rows, 1, s) : launch_sp<512, false, false>(c, lists, rows, 1, s);
 }
 

@@ -346,7 +346,7 @@ DMA_API dma_status_t dma_prologue_backward(const void* q, const void* k, int64_t
  *                     read as pages and may be anything; a needed entry outside
  *                     [0, num_pages) is reported as DMA_ERR_BAD_PAGE through dma_check
  * A sequence has at most max_pages * page_size tokens (at most 2^20); page_size
- * is any positive number (one that is a multiple of 4 lets the selection read dt
+ * is any positive number (one that is a multiple of 8 lets the selection read dt
  * 16 bytes at a time).  B <= 65536; K and V pools of up to 64 GiB each.
  *
  * dma_append_paged: [DMA steps 1-3] for the new tokens of a ragged batch, in one

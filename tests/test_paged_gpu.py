@@ -372,6 +372,68 @@ def test_decode_long_rows_split_over_a_cluster(dma, n, w, Hkv, dt):
     check_decode(x, out, w, 0, 0)
 
 
+def dt_pattern(kind, n, Hkv, gen):
+    """dt of n consecutive keys: [n, Hkv]."""
+    r = torch.rand((n, Hkv), generator=gen)
+    part = torch.rand((n, Hkv), generator=gen)
+    if kind == "half tied":                     # one value among others, above and below it
+        return torch.where(part < 0.5, torch.full_like(r, 0.75), r)
+    if kind == "tied under a few":              # all but one key in a hundred hold one value
+        return torch.where(part < 0.01, 0.5 + r, torch.full_like(r, 0.25))
+    if kind == "zeros":                         # most keys hold nothing
+        return torch.where(part < 0.99, torch.zeros(()), r)
+    if kind == "neighbours":                    # two values one bit apart
+        return torch.where(part < 0.5, torch.tensor(0.5), torch.nextafter(torch.tensor(0.5), torch.tensor(1.0)))
+    if kind == "tied at the end":               # the tied keys that count lie in the last ones
+        tied = torch.full((n, 1), 0.125).expand(n, Hkv).clone()
+        tied[-n // 50:] = 0.5
+        return tied
+    if kind == "lumps":                         # the best keys in random runs of four
+        lump = torch.rand((-(-n // 4), Hkv), generator=gen).repeat_interleave(4, 0)[:n]
+        return 0.01 * r + lump
+    assert kind == "one lane"                   # ... in every 32nd run of eight
+    return torch.where(((torch.arange(n) // 8) % 32 == 5)[:, None], 0.9 + 0.1 * r, 0.5 * r)
+
+
+@pytest.mark.parametrize("n,w,window,sinks,Hkv,page", [
+    (9001, 600, 0, 0, 2, 16),
+    (9001, 600, 8000, 13, 2, 16),               # ... under a window with sinks
+    (9001, 600, 8000, 13, 2, 5),                # pages that runs of eight cross
+    (60000, 2048, 0, 0, 1, 64),                 # a cluster per row
+    (60000, 2048, 50000, 100, 4, 20),
+])
+@pytest.mark.parametrize("kind", ["half tied", "tied under a few", "zeros", "neighbours", "tied at the end", "lumps", "one lane"])
+def test_decode_selection_of_hard_rows(dma, n, w, window, sinks, Hkv, page, kind):
+    x = decode_inputs([n, n - 7], Hkv, Hkv, 64, page, seed=n + Hkv, garbage=False)
+    gen = torch.Generator().manual_seed(n + w)
+    for b in range(2):
+        j = torch.arange(int(x["lens"][b]))
+        x["dt"][x["table"][b].long()[j // page], :, j % page] = dt_pattern(kind, len(j), Hkv, gen)
+    g = decode_gpu(x)
+    out, ws = run_decode(dma, g, w, window, sinks)
+    assert dma.dma_check(ws) == 0
+    check_lists(dma, x, ws, w, window, sinks)
+    check_decode(x, out, w, window, sinks)
+    again, _ = run_decode(dma, g, w, window, sinks)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("w,kind", [(2048, "lumps"), (2048, "half tied"), (8000, "lumps"), (8000, "zeros"), (8000, "one lane")])
+def test_decode_selection_of_many_rows(dma, w, kind):
+    """More rows than SMs, so that a row has one CTA, or a few for the lists of a large window."""
+    lens = [12000, 11111] + [9] * 90 + [w + 1, w, 12000]
+    x = decode_inputs(lens, 2, 2, 64, 16, seed=w, garbage=False)
+    gen = torch.Generator().manual_seed(w)
+    for b, n in enumerate(lens):
+        j = torch.arange(n)
+        x["dt"][x["table"][b].long()[j // 16], :, j % 16] = dt_pattern(kind, n, 2, gen)
+    g = decode_gpu(x)
+    out, ws = run_decode(dma, g, w)
+    assert dma.dma_check(ws) == 0
+    check_lists(dma, x, ws, w, 0, 0)
+    check_decode(x, out, w, 0, 0)
+
+
 def test_decode_long_row_kept_whole(dma):
     x = decode_inputs([40000, 3], 4, 2, 64, 16, seed=3, garbage=False)
     out, _ = run_decode(dma, decode_gpu(x), 1 << 20)
