@@ -55,7 +55,7 @@ struct DpArgs {
   uint16_t* out;
   float* warp_part;   // [blocks][warps][2][Hq / Hkv][piece_floats(d)]: o, m, l of the pieces at a warp range's ends
   float* block_part;  // [blocks][2][Hq / Hkv][piece_floats(d)]: the same for the blocks' ranges
-  uint32_t* tickets;  // [blocks], zero between calls: finished blocks of the row that begins in a block and leaves it
+  uint32_t* finished; // [blocks] bytes, zero between calls: finished blocks of the row that begins in a block and leaves it
   float scale;
   int Hq;
 };
@@ -569,10 +569,12 @@ __global__ void __launch_bounds__(DpCfg<D>::kThreads, 1) decode_paged_kernel(con
     uint32_t b0, b1;
     row_blocks(warp, b0, b1);
     // releases this block's pieces (written before the barrier) and acquires the others'
+    const uint32_t one = 1u << (8u * (b0 & 3u));
+    uint32_t* word = a.finished + (b0 >> 2);
     uint32_t before;
-    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.tickets + b0) : "memory");
-    if (before == b1 - b0) {
-      a.tickets[b0] = 0u;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(before) : "l"(word), "r"(one) : "memory");
+    if ((before / one & 255u) == b1 - b0) {
+      atomicSub(word, (b1 - b0 + 1u) * one);
       s_last[warp] = 1;
     }
   }
@@ -615,8 +617,8 @@ cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, cons
   a.k = static_cast<const uint16_t*>(k_pages);
   a.v = static_cast<const uint16_t*>(v_pages);
   a.out = static_cast<uint16_t*>(out);
-  a.tickets = static_cast<uint32_t*>(scratch);
-  a.block_part = reinterpret_cast<float*>(static_cast<char*>(scratch) + kPagedMaxBlocks * 4);
+  a.finished = c.err + kHdrRowWord;
+  a.block_part = static_cast<float*>(scratch);
   a.warp_part = a.block_part + kPagedMaxBlocks * 2 * psize;
   a.scale = scale;
   a.Hq = Hq;
@@ -625,8 +627,7 @@ cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, cons
 }
 
 size_t attn_paged_scratch_bytes(int Hq, int Hkv, int d) {
-  return kPagedMaxBlocks * 4 +
-         static_cast<size_t>(kPagedMaxBlocks) * (1 + kDpMaxWarps) * 2 * (Hq / Hkv) * piece_floats(d) * sizeof(float);
+  return static_cast<size_t>(kPagedMaxBlocks) * (1 + kDpMaxWarps) * 2 * (Hq / Hkv) * piece_floats(d) * sizeof(float);
 }
 
 }  // namespace dma

@@ -34,11 +34,16 @@ enum DeviceError : uint32_t {
 
 // Workspace header: status word at offset 0; the prefill attention's
 // work-item counter and finished-CTA counter at words kHdrItemWord and
-// kHdrDoneWord (the last CTA of each launch returns both to zero); the rest of
-// the first 256 bytes is reserved.
+// kHdrDoneWord (the last CTA of each launch returns both to zero); the finished
+// blocks of the prologue's backward at word kHdrPbWord and of the paged decode's
+// shared rows, a byte each, from word kHdrRowWord on (zero again after each
+// launch); the rest of the first 256 bytes is reserved.  Counters lie here, not in
+// an entry point's scratch, so that entry points can share a workspace.
 constexpr size_t kHeaderBytes = 256;
 constexpr int kHdrItemWord = 16;
 constexpr int kHdrDoneWord = 17;
+constexpr int kHdrPbWord = 18;
+constexpr int kHdrRowWord = 20;
 
 __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -105,8 +110,11 @@ struct PagedLists {
   int cap;
 };
 
-// Blocks that share a paged decode's work, at most (its scratch is sized for them).
-constexpr int kPagedMaxBlocks = 256;
+// Blocks that share a paged decode's work, at most (its scratch is sized for them,
+// and the header has a byte for each).
+constexpr int kPagedMaxBlocks = 160;
+static_assert(4 * kHdrRowWord + kPagedMaxBlocks <= static_cast<int>(kHeaderBytes), "row counters in the header");
+static_assert(kPagedMaxBlocks <= 255, "a row's finished blocks fit a byte");
 // Blocks of the prologue's backward, at most (a row of weight gradient shares each).
 constexpr int kPbMaxBlocks = 512;
 
@@ -131,7 +139,8 @@ struct PrologueBackward {
   void *dq, *dk;
   long long dq_stride, dk_stride;
   float *dq_norm_w, *dk_norm_w;
-  void* scratch;                  // prologue_backward_scratch_bytes, zeroed before its first use
+  float* part;                    // prologue_backward_scratch_bytes
+  uint32_t* ticket;               // finished blocks, zero between calls
   float eps, theta;
   int B, L, Hq, Hkv, d;
 };

@@ -175,10 +175,12 @@ dma_status_t dma_prologue_backward(const void* q, const void* k, int64_t q_strid
   if (static_cast<long long>(B) * L * Hq >= (1LL << 31)) return DMA_ERR_UNSUPPORTED;
   if (ws_bytes < dma_prologue_backward_workspace_size(B, L, Hq, Hkv, d)) return DMA_ERR_WORKSPACE;
   if ((st = device_ok()) != DMA_OK) return st;
-  void* scratch = static_cast<char*>(workspace) + kHeaderBytes;
-  const PrologueBackward p{q,  k,         q_stride,  k_stride,  q_norm_w,  k_norm_w, positions, dq_out, dk_out, dq,
-                           dk, dq_stride, dk_stride, dq_norm_w, dk_norm_w, scratch,  eps,       rope_theta, B,  L,
-                           Hq, Hkv,       d};
+  uint32_t* header = static_cast<uint32_t*>(workspace);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeaderBytes);
+  const PrologueBackward p{q,         k,         q_stride,  k_stride,  q_norm_w,   k_norm_w,
+                           positions, dq_out,    dk_out,    dq,        dk,         dq_stride,
+                           dk_stride, dq_norm_w, dk_norm_w, part,      header + kHdrPbWord,
+                           eps,       rope_theta, B,        L,         Hq,         Hkv,       d};
   const cudaError_t e = launch_prologue_backward(p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DMA_OK : cuda_fail(e);
 }

@@ -36,7 +36,6 @@ constexpr int kPbThreads = 256;
 constexpr int kPbWarps = kPbThreads / 32;
 constexpr int kPbMinBlocks = 2;
 constexpr int kPbStages = 4;                                     // ring steps per warp
-constexpr int kPbTicketBytes = 256;                              // one ticket
 constexpr int kPbSmemBytes = kPbWarps * kPbStages * 4 * 32 * 16;   // a step: four 16-byte chunks per lane
 
 struct PbArgs {
@@ -262,8 +261,8 @@ cudaError_t launch_prologue_backward(const PrologueBackward& p, cudaStream_t s) 
   a.dk = static_cast<uint16_t*>(p.dk);
   a.dq_w = p.dq_norm_w;
   a.dk_w = p.dk_norm_w;
-  a.ticket = static_cast<uint32_t*>(p.scratch);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(p.scratch) + kPbTicketBytes);
+  a.ticket = p.ticket;
+  a.part = p.part;
   a.eps = p.eps;
   a.L = p.L;
   const int slots = std::min(kPbMinBlocks * nsm, kPbMaxBlocks);
@@ -277,7 +276,7 @@ cudaError_t launch_prologue_backward(const PrologueBackward& p, cudaStream_t s) 
 }
 
 size_t prologue_backward_scratch_bytes(int d) {
-  return kPbTicketBytes + static_cast<size_t>(kPbMaxBlocks) * 2 * d * sizeof(float);
+  return static_cast<size_t>(kPbMaxBlocks) * 2 * d * sizeof(float);
 }
 
 }  // namespace dma

@@ -36,8 +36,10 @@
  *     recorded in the workspace's status word; read them with dma_check().
  *   - A workspace must be zeroed once before its first use.  Its first 256
  *     bytes are a header: the status word at byte 0 (kernels only ever set
- *     it) and, at bytes 64-71, a work-item counter of the d = 128 prefill
- *     attention, which every such call leaves at zero when it ends.
+ *     it) and counters that every call leaves at zero when it ends: at bytes
+ *     64-71 of the d = 128 prefill attention, at bytes 72-75 of
+ *     dma_prologue_backward, at bytes 80-239 of dma_decode_paged.  Calls in
+ *     stream order may share a workspace, whatever their entry points.
  *   - Calls on different streams must use different workspaces.
  */
 #ifndef DMA_H_

@@ -434,6 +434,32 @@ def test_decode_selection_of_many_rows(dma, w, kind):
     check_decode(x, out, w, 0, 0)
 
 
+@pytest.mark.parametrize("d,lens,w", [(64, [700, 3, 90, 4000], 2048), (128, [2500, 0, 31], 300), (64, [9000], 64)])
+def test_workspace_that_held_something_else(dma, d, lens, w):
+    """Only the header has to be zero: entry points share a workspace, whatever they left behind it."""
+    x = decode_inputs(lens, 8, 4, d, 16, seed=d + w, garbage=False)
+    g = decode_gpu(x)
+    want, _ = run_decode(dma, g, w)
+    size = dma.dma_decode_paged_workspace_size(len(lens), g["table"].shape[1], 16, 8, 4, d, w)
+    ws = dma.new_workspace(max(size, dma.dma_prologue_backward_workspace_size(2, 40, 8, 4, d)))
+    q, k = (torch.randn((2, 40, h, d), device="cuda").bfloat16() for h in (8, 4))
+    dq, dk = torch.randn_like(q), torch.randn_like(k)
+    one = torch.ones(d, device="cuda")
+    back = lambda ws=None: dma.dma_prologue_backward(q, k, one, one, torch.zeros(2, dtype=torch.int32, device="cuda"), dq,
+                                                     dk, workspace=ws)
+    grads = back()
+    for fill in (0xFF, 0x01, None):
+        if fill is not None:
+            ws[256:] = fill
+        for _ in range(2):
+            out = dma.dma_decode_paged(g["q"], g["k"], g["v"], g["dt"], g["table"], g["lens"], w, workspace=ws)
+            assert torch.equal(out, want)
+            assert not ws[:256].any()
+            for a, b in zip(back(ws), grads):
+                assert torch.equal(a, b)
+            assert not ws[:256].any()
+
+
 def test_decode_long_row_kept_whole(dma):
     x = decode_inputs([40000, 3], 4, 2, 64, 16, seed=3, garbage=False)
     out, _ = run_decode(dma, decode_gpu(x), 1 << 20)
