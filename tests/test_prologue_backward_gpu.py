@@ -41,19 +41,19 @@ def inputs(B, L, Hq, Hkv, d, positions, seed, small_rows=False):
     return x
 
 
-def check(x, dq, dk, dqw, dkw, theta):
+def check(x, dq, dk, dqw, dkw, theta, eps=1e-6):
     p = x["positions"].numpy()
-    want = oracle.prologue_backward(f64(x["q"]), f64(x["k"]), f64(x["q_w"]), f64(x["k_w"]), 1e-6, theta, p,
+    want = oracle.prologue_backward(f64(x["q"]), f64(x["k"]), f64(x["q_w"]), f64(x["k_w"]), eps, theta, p,
                                     f64(x["dq_out"]), f64(x["dk_out"]))
     for got, ref, inp, w, g, what in ((dq, want[0], "q", "q_w", "dq_out", "dq"), (dk, want[1], "k", "k_w", "dk_out", "dk")):
-        r = 1 / np.sqrt((f64(x[inp]) ** 2).mean(-1, keepdims=True) + 1e-6)
+        r = 1 / np.sqrt((f64(x[inp]) ** 2).mean(-1, keepdims=True) + eps)
         size = r * np.linalg.norm(f64(x[g]) * f64(x[w]).max(), axis=-1, keepdims=True)
         err = np.abs(f64(got) - ref)
         assert np.isfinite(f64(got)).all()
         assert (err <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -18 * size).all(), f"{what}: {err.max():.3e}"
     for got, ref, inp, g, what in ((dqw, want[2], "q", "dq_out", "dq_norm_w"), (dkw, want[3], "k", "dk_out", "dk_norm_w")):
         xi = f64(x[inp])
-        xh = xi / np.sqrt((xi ** 2).mean(-1, keepdims=True) + 1e-6)
+        xh = xi / np.sqrt((xi ** 2).mean(-1, keepdims=True) + eps)
         terms = np.stack([np.abs(oracle.rope(f64(x[g])[b], -(int(p[b]) + np.arange(xi.shape[1])), theta) * xh[b]).sum((0, 1))
                           for b in range(len(p))]).sum(0)
         # the angles' float32 error turns a channel pair into itself: the partner's term counts as well
@@ -83,6 +83,15 @@ def test_matches_oracle(dma, B, L, Hq, Hkv, d, positions, theta):
     check(x, *r, theta)
     for a, b in zip(r, call()):
         assert torch.equal(a, b)                              # the same call, the same bits
+
+
+@pytest.mark.parametrize("B,L,Hq,Hkv,d", [(1, 3, 3, 1, 64), (3, 7, 5, 1, 128), (1, 33, 6, 2, 64), (1, 1, 1, 1, 64)])
+def test_without_eps(dma, B, L, Hq, Hkv, d):
+    """eps = 0: heads and tokens that fill up a warp's step must not add to the weights' gradients."""
+    x = inputs(B, L, Hq, Hkv, d, list(range(B)), seed=d + L)
+    g = {n: t.cuda() for n, t in x.items()}
+    r = dma.dma_prologue_backward(g["q"], g["k"], g["q_w"], g["k_w"], g["positions"], g["dq_out"], g["dk_out"], eps=0.0)
+    check(x, *r, 10000.0, eps=0.0)
 
 
 def test_slices_of_projection_buffers(dma):
