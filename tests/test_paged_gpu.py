@@ -600,6 +600,72 @@ def test_calls_on_another_stream(dma):
     check_decode(x, out, 100, 0, 0)
 
 
+def test_append_and_decode_in_one_graph(dma):
+    """A serving step captured once: packed tokens of other sequences, positions and padding on every replay."""
+    Hq, Hkv, d, page, T, B = 8, 4, 64, 16, 12, 4
+    runs = [([1, 1, 1, 1], [0, 15, 40, 63]), ([3, 0, 1, 8], [2, 9, 79, 16]), ([0, 0, 0, 1], [1, 2, 3, 0])]
+    xs = [append_inputs(n, p, Hq, Hkv, d, page, pad=T - sum(n), seed=i, max_pages=5) for i, (n, p) in enumerate(runs)]
+    n_pages = max(x["k_pages"].shape[0] for x in xs)
+    g = on_gpu(xs[0])
+    for n in ("k_pages", "v_pages", "dt_pages"):
+        g[n] = torch.zeros((n_pages,) + tuple(xs[0][n].shape[1:]), dtype=xs[0][n].dtype, device="cuda")
+    lens, last = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int64, device="cuda")
+    q_out = torch.zeros((T, Hq, d), dtype=torch.bfloat16, device="cuda")
+    rows, out = torch.zeros((B, Hq, d), dtype=torch.bfloat16, device="cuda"), torch.zeros((B, Hq, d), dtype=torch.bfloat16, device="cuda")
+    ws = dma.new_workspace(dma.dma_decode_paged_workspace_size(B, 5, page, Hq, Hkv, d, 20))
+
+    def step():
+        dma.dma_append_paged(g["q"], g["k"], g["v"], g["q_w"], g["k_w"], g["W"], g["A"], g["cu"], g["positions"],
+                             g["table"], g["k_pages"], g["v_pages"], g["dt_pages"], q_out=q_out, workspace=ws)
+        torch.index_select(q_out, 0, last, out=rows)
+        dma.dma_decode_paged(rows, g["k_pages"], g["v_pages"], g["dt_pages"], g["table"], lens, 20, out=out, workspace=ws)
+
+    g["cu"].zero_()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in (0, 1, 2, 0):
+        x, (news, positions) = xs[i], runs[i]
+        q_out.fill_(77.0)
+        for n in ("q", "k", "v", "q_w", "k_w", "W", "A", "cu", "positions", "table"):
+            g[n].copy_(x[n].cuda())
+        for n in ("k_pages", "v_pages", "dt_pages"):
+            g[n][:x[n].shape[0]] = x[n].cuda()
+        lens.copy_(torch.tensor([p + n if n else 0 for n, p in zip(news, positions)], dtype=torch.int32))
+        last.copy_((x["cu"][1:] - 1).clamp(min=0))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert dma.dma_check(ws) == 0
+        pools = {n: g[n][:x[n].shape[0]].clone() for n in ("k_pages", "v_pages", "dt_pages")}
+        check_append(x, pools, q_out, None)
+        state = {"q": rows.cpu(), "k": pools["k_pages"].cpu(), "v": pools["v_pages"].cpu(), "dt": pools["dt_pages"].cpu(),
+                 "table": x["table"], "lens": lens.cpu()}
+        check_decode(state, out, 20, 0, 0)
+
+
+def test_two_decodes_at_once(dma):
+    """Calls on two streams, each with its own workspace, over the same pages."""
+    x = decode_inputs([9000, 70, 3000], 8, 4, 64, 16, seed=41, garbage=False)
+    g = decode_gpu(x)
+    want = {w: run_decode(dma, g, w)[0] for w in (300, 2048)}
+    streams = {w: torch.cuda.Stream() for w in want}
+    ws = {w: dma.new_workspace(dma.dma_decode_paged_workspace_size(3, g["table"].shape[1], 16, 8, 4, 64, w)) for w in want}
+    torch.cuda.synchronize()
+    got = {w: [] for w in want}
+    for _ in range(20):
+        for w in want:
+            got[w].append(dma.dma_decode_paged(g["q"], g["k"], g["v"], g["dt"], g["table"], g["lens"], w, workspace=ws[w],
+                                               stream=streams[w]))
+    torch.cuda.synchronize()
+    for w in want:
+        for out in got[w]:
+            assert torch.equal(out, want[w])
+
+
 def test_prompt_then_decode_steps(dma):
     """A user's run: prompts enter the pages (and prefill reads their rotated keys), then single tokens are appended
     and decoded; every decode output against the oracle over what the pages hold, the first also against the
