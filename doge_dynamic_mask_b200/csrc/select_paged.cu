@@ -21,11 +21,13 @@
 // passes.  The order of the list is fixed by the row alone, so the attention adds
 // its terms in the same order every time.
 //
-// What bounds it: integer instructions and the latency of its steps, not the one
-// read of dt.  512 rows of 32k to 64k keys, w = 2048: about 50 us for 100 MB (16 us
-// at the copy rate); in cycles of a CTA of 512 threads: sample 6k, threshold 3k,
-// collection 27k, bins 6k, writing 7k.  Lists per warp built with votes at 256
-// threads took 77k cycles a CTA, four CTAs an SM instead of two: the same time.
+// What bounds it: the latency and the integer instructions of its steps rather
+// than the one read of dt.  512 rows of 32k to 64k keys, w = 2048: about 58 us for
+// 100 MB (16 us at the copy rate); in cycles of a CTA of 512 threads, two CTAs an
+// SM: sample 6k, threshold 3k, collection 24k (near the copy rate while it lasts),
+// bins 4k, edge 4k, writing 5k.  Lists per warp built with votes at 256 threads, four
+// CTAs an SM, took 77k cycles a CTA: the same time.  Starting the collection's
+// loads before the sample only made the sample wait for them.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -458,14 +460,15 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
   const int xw = min(r.no, (rank * (THREADS / 32) + warp) * part), xe = min(r.no, xw + part);
   {
     int page[Cfg::kUnroll];
+    uint32_t v[Cfg::kUnroll][8], seen[Cfg::kUnroll];
 #pragma unroll
     for (int u = 0; u < Cfg::kUnroll; ++u) page[u] = oct_page(c, r, xw + lane + 32 * u, xe);
+#pragma unroll
+    for (int u = 0; u < Cfg::kUnroll; ++u) {
+      seen[u] = load_oct<VEC>(c, r, xw + lane + 32 * u, page[u], v[u], xe);
+      page[u] = oct_page(c, r, xw + lane + 32 * (Cfg::kUnroll + u), xe);
+    }
     for (int x = xw + lane; x < xe; x += 32 * Cfg::kUnroll) {
-      uint32_t v[Cfg::kUnroll][8], seen[Cfg::kUnroll];
-#pragma unroll
-      for (int u = 0; u < Cfg::kUnroll; ++u) seen[u] = load_oct<VEC>(c, r, x + 32 * u, page[u], v[u], xe);
-#pragma unroll
-      for (int u = 0; u < Cfg::kUnroll; ++u) page[u] = oct_page(c, r, x + 32 * (Cfg::kUnroll + u), xe);
 #pragma unroll
       for (int u = 0; u < Cfg::kUnroll; ++u) {
         if (seen[u] != 255u) {
@@ -490,12 +493,26 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
             atomicAdd(&sm.hist[bin_of(bits)], 1u);
           }
         }
+        // the next oct of this place travels while the others are looked through
+        seen[u] = load_oct<VEC>(c, r, x + 32 * (Cfg::kUnroll + u), page[u], v[u], xe);
+        page[u] = oct_page(c, r, x + 32 * (2 * Cfg::kUnroll + u), xe);
       }
     }
   }
   const int n = static_cast<int>((at - first) / kStep);   // this thread's keys
-  auto key_bits = [&](int i) { return list[2 * i * THREADS + tid]; };
   auto key_pos = [&](int i) { return static_cast<int>(list[(2 * i + 1) * THREADS + tid]); };
+  // f(i, bits, bin) for each of them, four read at a time (the slack rows follow the last)
+  auto each_key = [&](auto&& f) {
+    static_assert(Cfg::kSlack >= 3, "reads past a full list");
+    for (int i0 = 0; i0 < n; i0 += 4) {
+      uint32_t bits[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bits[i] = list[2 * (i0 + i) * THREADS + tid];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i0 + i < n) f(i0 + i, bits[i], static_cast<int>(bin_of(bits[i])));
+    }
+  };
   {
     const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(n));
     n_tied = __reduce_add_sync(0xFFFFFFFFu, n_tied);
@@ -504,7 +521,7 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
       atomicAdd(&sm.ties, n_tied);
       sm.warp[2][warp] = n_tied;
     }
-    for (int i = 0; i < n; ++i) atomicAdd(&sm.hist[bin_of(key_bits(i))], 1u);
+    each_key([&](int, uint32_t, int bin) { atomicAdd(&sm.hist[bin], 1u); });
   }
 
   // ---- the w-th key's bin, over the cluster
@@ -545,12 +562,10 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
   if (!bad) {
     // keys inside the bin go to the first CTA (they are ranked by value, so
     // their order there does not matter); keys above it are counted
-    for (int i = 0; i < n; ++i) {
-      const uint32_t bits = key_bits(i);
-      const int bin = static_cast<int>(bin_of(bits));
+    each_key([&](int i, uint32_t bits, int bin) {
       before += bin > wbin;
       if (bin == wbin) lead->edge[atomicAdd(&lead->edges, 1u)] = composite_key(bits, key_pos(i));
-    }
+    });
     if (tid < sm.spills) {
       const uint64_t key = sm.spill[tid];
       const int bin = static_cast<int>(bin_of(static_cast<uint32_t>(key >> 32)));
@@ -574,10 +589,9 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
     uint32_t start = 0;
     for (int q = 0; q < rank; ++q) start += of_rank(q)->sure;
     uint32_t pos = start + warps_before(sm.warp[1]) + before;
-    for (int i = 0; i < n; ++i) {
-      const uint32_t bits = key_bits(i);
-      if (static_cast<int>(bin_of(bits)) > wbin) out.put(pos++, static_cast<int>(key_pos(i)), bits);
-    }
+    each_key([&](int i, uint32_t bits, int bin) {
+      if (bin > wbin) out.put(pos++, key_pos(i), bits);
+    });
     // then the spilled ones, in the order of their positions
     const uint32_t spills = sm.spills;
     const uint64_t key = tid < spills ? sm.spill[tid] : 0ull;
