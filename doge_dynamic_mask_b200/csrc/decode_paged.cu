@@ -13,7 +13,7 @@
 // per 2 bytes.  All rows of all sequences and kv heads form one axis of 16-key
 // tiles, and the blocks of the grid, and their warps, take equal contiguous
 // ranges of it, so ragged batches and single long sequences fill the SMs
-// alike.  A warp that begins or ends inside a row leaves a float32 piece (o, m,
+// alike (few rows of like lengths get a block each).  A warp that begins or ends inside a row leaves a float32 piece (o, m,
 // l); a block joins its warps' pieces, and of the blocks that share a row the
 // last one to finish joins theirs, always in the order of the axis.  A warp
 // works alone: its tiles travel by cp.async through a ring of its own (keys
@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kDpMaxWarps = 16;
 constexpr int kTileKeys = 16;
+constexpr uint32_t kRowSteps = 3;   // tiles of a warp that cost less than joining a row's blocks
 constexpr float kLog2e = 1.4426950408889634f;
 
 // d = 128 takes 204 registers a thread: eight warps, 25 KB of ring each.  d = 64
@@ -218,6 +219,7 @@ __global__ void __launch_bounds__(DpCfg<D>::kThreads, 1) decode_paged_kernel(con
   // counts for itself, four sequences per lane at a time.
   constexpr int kSeqs = 128;
   uint32_t tiles[4], upto = 0;   // of this lane's sequences of a step; of the step up to and with them
+  uint32_t most = 0;             // of any of this lane's sequences
   auto count_step = [&](int b0) {   // returns the step's tiles
     upto = 0;
 #pragma unroll
@@ -225,6 +227,7 @@ __global__ void __launch_bounds__(DpCfg<D>::kThreads, 1) decode_paged_kernel(con
       const int b = b0 + 4 * lane + i;
       tiles[i] = b < c.B ? static_cast<uint32_t>(seq_tiles(c, b)) : 0u;
       upto += tiles[i];
+      most = max(most, tiles[i]);
     }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -236,17 +239,26 @@ __global__ void __launch_bounds__(DpCfg<D>::kThreads, 1) decode_paged_kernel(con
   uint32_t total = 0;
   for (int b0 = 0; b0 < c.B; b0 += kSeqs) total += count_step(b0);
   const uint32_t U = total * static_cast<uint32_t>(c.Hkv);
-  const uint32_t G = min(gridDim.x, (U + kDpWarps - 1u) / kDpWarps);
+  // few rows of like lengths: a block takes a row (its part of the axis begins at 0
+  // then), and none joins with others.  48 sequences that see 1028 keys of 2 heads of
+  // 128 took 20.5 us over equal parts, 17.4 us so; one of 301 keys of 4 heads of 64,
+  // 9.0 and 7.5 us; at five tiles a warp instead of kRowSteps both are alike.
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  const uint32_t rows = static_cast<uint32_t>(c.B) * static_cast<uint32_t>(c.Hkv);
+  const bool by_row = rows <= gridDim.x && most * gridDim.x <= U + kRowSteps * kDpWarps * gridDim.x;
+  const uint32_t G = by_row ? rows : min(gridDim.x, (U + kDpWarps - 1u) / kDpWarps);
   if (blockIdx.x >= G) return;
   const Axis axis(U, G);
-  const uint32_t xb0 = axis.begin(blockIdx.x), xb1 = axis.begin(blockIdx.x + 1u), nb = xb1 - xb0;
-  auto warp_begin = [&](uint32_t w) { return xb0 + nb * w / kDpWarps; };
-  const uint32_t x0 = warp_begin(warp);
-  const int count = static_cast<int>(warp_begin(warp + 1) - x0);
+  const int hshift = 31 - __clz(c.Hkv);   // (Hkv is a power of two)
   Cursor cur{};
-  {
-    const uint32_t y = x0 >> (31 - __clz(c.Hkv));   // (Hkv is a power of two) tiles of sequences before x0's, rounded into it
-    uint32_t before = 0;
+  uint32_t xb0 = 0u, nb = 0u, before = 0u;
+  auto warp_begin = [&](uint32_t w) { return xb0 + nb * w / kDpWarps; };
+  if (by_row) {
+    cur.b = static_cast<int>(blockIdx.x) >> hshift;
+  } else {
+    xb0 = axis.begin(blockIdx.x);
+    nb = axis.begin(blockIdx.x + 1u) - xb0;
+    const uint32_t y = warp_begin(warp) >> hshift;   // tiles of sequences before the warp's first one, rounded into it
     for (int b0 = 0; b0 < c.B; b0 += kSeqs) {
       const uint32_t next = c.B > kSeqs ? before + count_step(b0) : total;
       if (y >= next) {
@@ -267,7 +279,15 @@ __global__ void __launch_bounds__(DpCfg<D>::kThreads, 1) decode_paged_kernel(con
       }
       break;
     }
-    cur.enter(c);
+  }
+  cur.enter(c);
+  if (by_row) nb = static_cast<uint32_t>(cur.nt);
+  const uint32_t xb1 = xb0 + nb, x0 = warp_begin(warp);
+  const int count = static_cast<int>(warp_begin(warp + 1) - x0);
+  if (by_row) {
+    cur.g = static_cast<int>(blockIdx.x) & (c.Hkv - 1);
+    cur.t = static_cast<int>(x0);
+  } else {
     const uint32_t rem = x0 - before * static_cast<uint32_t>(c.Hkv);
     cur.g = static_cast<int>(rem / static_cast<uint32_t>(cur.nt));
     cur.t = static_cast<int>(rem) - cur.g * cur.nt;

@@ -319,8 +319,11 @@ def _refuse(device, *wanted):
 
 def _token_stride(name, t):
     """Elements between tokens of [.., H, d] whose head rows are dense (a slice of a wider projection's output)."""
-    shape, st = t.shape, t.stride()
+    shape = t.shape
     d = shape[-1]
+    if t.is_contiguous():
+        return shape[-2] * d
+    st = t.stride()
     if st[-1] != 1 or (shape[-2] > 1 and st[-2] != d):
         raise ValueError(f"{name}: its heads must be dense")
     if len(st) == 3:
@@ -333,6 +336,8 @@ def _token_stride(name, t):
 def _page_stride(k_pages, v_pages):
     """Elements between the pages of both pools (the rest of a page is dense)."""
     _, page_size, Hkv, d = shape = k_pages.shape
+    if k_pages.is_contiguous() and v_pages.is_contiguous() and v_pages.shape == shape:
+        return page_size * Hkv * d
     st = k_pages.stride()
     if (v_pages.shape != shape or v_pages.stride() != st or st[3] != 1 or (Hkv > 1 and st[2] != d)
             or (page_size > 1 and st[1] != Hkv * d)):
