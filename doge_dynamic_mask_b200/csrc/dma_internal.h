@@ -98,6 +98,7 @@ struct PagedCache {
   long long page_stride16;        // 16-byte units between pages of k_pages / v_pages
   int B, max_pages, num_pages, page_size;
   int page_shift;                 // log2(page_size), or -1
+  float page_inv;                 // 1 / page_size
   int Hkv, d, w, window, sinks;   // window 0: every key below the length is visible
   uint32_t* err;
 };

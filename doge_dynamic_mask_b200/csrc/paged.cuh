@@ -27,15 +27,22 @@ __device__ __forceinline__ int key_position(const PagedCache& c, const SeqView& 
   return v.shift > 0 && i >= c.sinks ? i + v.shift : i;
 }
 
-// position -> (page slot of the table, row of the page)
+// position -> (page slot of the table, row of the page).  Positions lie below 2^20, so
+// the product with the reciprocal is off by less than a quarter of 1 / page_size:
+// its whole part is the slot, or one below it where the position begins a page.
 __device__ __forceinline__ int page_slot(const PagedCache& c, int j, int& off) {
   int slot;
   if (c.page_shift >= 0) {
     slot = j >> c.page_shift;
+    off = j - slot * c.page_size;
   } else {
-    slot = static_cast<int>(static_cast<unsigned>(j) / static_cast<unsigned>(c.page_size));
+    slot = static_cast<int>(static_cast<float>(j) * c.page_inv);
+    off = j - slot * c.page_size;
+    if (off >= c.page_size) {
+      off -= c.page_size;
+      ++slot;
+    }
   }
-  off = j - slot * c.page_size;
   return slot;
 }
 

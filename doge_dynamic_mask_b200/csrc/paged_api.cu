@@ -133,6 +133,7 @@ dma_status_t dma_decode_paged(const void* q, const void* k_pages, const void* v_
   c.num_pages = num_pages;
   c.page_size = page_size;
   c.page_shift = -1;
+  c.page_inv = 1.0f / static_cast<float>(page_size);
   for (int i = 0; i <= 20; ++i)
     if (page_size == 1 << i) c.page_shift = i;
   c.Hkv = Hkv;

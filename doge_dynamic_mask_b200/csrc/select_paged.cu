@@ -162,6 +162,45 @@ __device__ __forceinline__ uint32_t load_oct(const PagedCache& c, const Row& r, 
   return seen;
 }
 
+// A step of the collection: 32 octs from q0 on, eight keys of them per lane.  VEC:
+// an oct a lane; else lane l has every 32nd key from the l-th on, so that a load
+// of the warp reads neighbouring keys (64 sequences of 32k to 64k keys in pages of
+// five, the step with its attention: 480 us with an oct a lane, 277 us so; in pages
+// of 100, 208 and 223 us).
+template <bool VEC>
+__device__ __forceinline__ int step_position(const Row& r, int q0, int e) {
+  const int lane = threadIdx.x & 31;
+  return VEC ? oct_position(r, q0 + lane) + e : oct_position(r, q0 + 4 * e + (lane >> 3)) + (lane & 7);
+}
+
+// dt bits of this lane's keys of a step, 0 for those that are not seen.  page: the
+// table entry of its oct (VEC).
+template <bool VEC>
+__device__ __forceinline__ uint32_t load_step(const PagedCache& c, const Row& r, int q0, int page, uint32_t (&v)[8],
+                                              int end) {
+  const int lane = threadIdx.x & 31;
+  uint32_t seen = 0u;
+  if constexpr (VEC) {
+    seen = load_oct<true>(c, r, q0 + lane, page, v, end);
+  } else {
+    int pages[8], offs[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int x = q0 + 4 * e + (lane >> 3), j = oct_position(r, x) + (lane & 7);
+      const bool there = x < end && (x < r.noa ? j < r.sinks : j >= r.start && j < r.len);
+      seen |= there ? 1u << e : 0u;
+      const int slot = page_slot(c, there ? j : 0, offs[e]);
+      pages[e] = there ? __ldg(r.table + slot) : 0;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if ((seen >> e & 1u) && checked_page(c, pages[e]) < 0) seen &= ~(1u << e);
+      v[e] = seen >> e & 1u ? __float_as_uint(__ldg(c.dt_pages + dt_offset(c, pages[e], offs[e], r.g))) : 0u;
+    }
+  }
+  return seen;
+}
+
 // A row's kept list.
 struct Kept {
   int32_t* pos;
@@ -462,16 +501,16 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
     int page[Cfg::kUnroll];
     uint32_t v[Cfg::kUnroll][8], seen[Cfg::kUnroll];
 #pragma unroll
-    for (int u = 0; u < Cfg::kUnroll; ++u) page[u] = oct_page(c, r, xw + lane + 32 * u, xe);
+    for (int u = 0; u < Cfg::kUnroll; ++u) page[u] = VEC ? oct_page(c, r, xw + lane + 32 * u, xe) : 0;
 #pragma unroll
     for (int u = 0; u < Cfg::kUnroll; ++u) {
-      seen[u] = load_oct<VEC>(c, r, xw + lane + 32 * u, page[u], v[u], xe);
-      page[u] = oct_page(c, r, xw + lane + 32 * (Cfg::kUnroll + u), xe);
+      seen[u] = load_step<VEC>(c, r, xw + 32 * u, page[u], v[u], xe);
+      if (VEC) page[u] = oct_page(c, r, xw + lane + 32 * (Cfg::kUnroll + u), xe);
     }
-    for (int x = xw + lane; x < xe; x += 32 * Cfg::kUnroll) {
+    for (int q0 = xw; q0 < xe; q0 += 32 * Cfg::kUnroll) {
 #pragma unroll
       for (int u = 0; u < Cfg::kUnroll; ++u) {
-        if (seen[u] != 255u) {
+        if (VEC && seen[u] != 255u) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[u][e] = seen[u] >> e & 1u ? v[u][e] : 0u;
         }
@@ -479,11 +518,12 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
 #pragma unroll
           for (int e = 0; e < 8; ++e) n_tied += (seen[u] >> e & 1u) && v[u][e] == tie;
         }
-        const uint32_t j0 = static_cast<uint32_t>(oct_position(r, x + 32 * u));
+        const int qu = q0 + 32 * u, j0 = step_position<VEC>(r, qu, 0);
 #pragma unroll
         for (int e0 = 0; e0 < 8; e0 += Cfg::kSlack) {
 #pragma unroll
-          for (int e = e0; e < e0 + Cfg::kSlack; ++e) append_if<THREADS>(at, v[u][e], j0 + e, thr);
+          for (int e = e0; e < e0 + Cfg::kSlack; ++e)
+            append_if<THREADS>(at, v[u][e], VEC ? j0 + e : step_position<VEC>(r, qu, e), thr);
           for (; at > full; at -= kStep) {   // the keys in the slack rows move to the CTA's spill
             const uint32_t last = (at - first) / kStep - 1u;
             const uint32_t bits = list[2 * last * THREADS + tid], pos = list[(2 * last + 1) * THREADS + tid];
@@ -493,9 +533,9 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
             atomicAdd(&sm.hist[bin_of(bits)], 1u);
           }
         }
-        // the next oct of this place travels while the others are looked through
-        seen[u] = load_oct<VEC>(c, r, x + 32 * (Cfg::kUnroll + u), page[u], v[u], xe);
-        page[u] = oct_page(c, r, x + 32 * (2 * Cfg::kUnroll + u), xe);
+        // this place's next keys travel while the others are looked through
+        seen[u] = load_step<VEC>(c, r, qu + 32 * Cfg::kUnroll, page[u], v[u], xe);
+        if (VEC) page[u] = oct_page(c, r, qu + lane + 64 * Cfg::kUnroll, xe);
       }
     }
   }
