@@ -39,6 +39,11 @@
 // fragments of its 128 channels in registers for all of its tokens.  The
 // projection is 2 Hkv flops per byte of V: far below what tcgen05 is for, and a
 // 128-row tile would leave a decode step's few tokens on one SM.
+//
+// Measured.  32768 tokens, 16 + 8 heads of 128, K rows packed as well: 108 us for
+// 605 MB, 5.6 TB/s (94 us at the copy rate).  9 prompts of up to 2047 tokens, 8 + 4
+// heads of 64: 11.8 us for 43 MB, of which about 4 us are the start and W's split.
+// 57 single tokens: 5.6 us, a launch and four dependent memory latencies.
 #include <algorithm>
 
 #include "rope.cuh"
@@ -136,7 +141,7 @@ struct ApCfg {
   static constexpr int NT = HKV > 8 ? 2 : 1;                // groups of eight heads
   static constexpr int kWarps = kSlices > 8 ? 16 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kMinBlocks = kWarps > 8 ? 1 : NT > 1 ? 2 : 2;
+  static constexpr int kMinBlocks = kWarps > 8 ? 1 : 2;
   static constexpr int kTiles = kWarps / kSlices;           // 16-token tiles of a block at once
   static constexpr int LPR = D / 16;
   static constexpr int kStages = 6;                         // ring steps per warp: two 16-byte chunks per lane each
