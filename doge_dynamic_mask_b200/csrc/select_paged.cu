@@ -27,7 +27,9 @@
 // SM: sample 6k, threshold 3k, collection 24k (near the copy rate while it lasts),
 // bins 4k, edge 4k, writing 5k.  Lists per warp built with votes at 256 threads, four
 // CTAs an SM, took 77k cycles a CTA: the same time.  Starting the collection's
-// loads before the sample only made the sample wait for them.
+// loads before the sample only made the sample wait for them.  One row of 500k keys
+// on a cluster: 17 us; counting into the first CTA's histogram by remote atomics,
+// instead of adding the CTAs' histograms there, took 2 us more.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -44,6 +46,7 @@ namespace cg = cooperative_groups;
 constexpr int kSpSample = 512;           // sampled octs (runs of eight positions), at most
 constexpr int kSpSampleLong = 131072;    // rows up to this length take half of them
 constexpr int kSpEdge = 512;             // keys inside the w-th key's bin
+constexpr int kSpMaxCluster = 8;         // CTAs of a row
 constexpr int kSpSpill = 128;            // keys of a CTA that found their thread's list full
 // many rows: 512 threads, two CTAs per SM; rows split over a cluster: 1024
 // threads, one CTA per SM
@@ -566,13 +569,15 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
 
   // ---- the w-th key's bin, over the cluster
   sync_all();
-  uint32_t bad = 0, total = 0, ties = 0, ties_before = 0;   // ..before: in the CTAs before this one
-  for (int q = 0; q < csize; ++q) {
-    const SpShared* other = of_rank(q);
-    bad |= other->spills > static_cast<uint32_t>(kSpSpill);
-    total += other->keys;
-    ties += other->ties;
-    if (q < rank) ties_before += other->ties;
+  uint32_t bad, total, ties, ties_before;   // ..before: in the CTAs before this one
+  {
+    const SpShared* other = of_rank(min(lane, csize - 1));   // a CTA a lane
+    const bool in = lane < csize;
+    const uint32_t spills = other->spills, keys = other->keys, tied_keys = other->ties;
+    bad = __any_sync(0xFFFFFFFFu, spills > static_cast<uint32_t>(kSpSpill));
+    total = __reduce_add_sync(0xFFFFFFFFu, in ? keys : 0u);
+    ties = __reduce_add_sync(0xFFFFFFFFu, in ? tied_keys : 0u);
+    ties_before = __reduce_add_sync(0xFFFFFFFFu, lane < rank ? tied_keys : 0u);
   }
   // keys of the tied value that the list still has room for
   const uint32_t fill = total < static_cast<uint32_t>(w) ? static_cast<uint32_t>(w) - total : 0u;
@@ -584,10 +589,16 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
         sm, static_cast<uint32_t>(w),
         [&](int i) {
           uint2 s = make_uint2(0u, 0u);
-          for (int q = 1; q < csize; ++q) {
-            const uint2 y = *reinterpret_cast<const uint2*>(of_rank(q)->hist + i);
-            s.x += y.x;
-            s.y += y.y;
+          if (CLUSTER) {
+            uint2 y[kSpMaxCluster];   // all on their way at once
+#pragma unroll
+            for (int q = 1; q < kSpMaxCluster; ++q)
+              y[q] = q < csize ? *reinterpret_cast<const uint2*>(of_rank(q)->hist + i) : make_uint2(0u, 0u);
+#pragma unroll
+            for (int q = 1; q < kSpMaxCluster; ++q) {
+              s.x += y[q].x;
+              s.y += y[q].y;
+            }
           }
           return s;
         },
@@ -626,8 +637,8 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
   }
   sync_all();
   if (!bad) {
-    uint32_t start = 0;
-    for (int q = 0; q < rank; ++q) start += of_rank(q)->sure;
+    const uint32_t sure = of_rank(min(lane, csize - 1))->sure;
+    const uint32_t start = __reduce_add_sync(0xFFFFFFFFu, lane < rank ? sure : 0u);
     uint32_t pos = start + warps_before(sm.warp[1]) + before;
     each_key([&](int i, uint32_t bits, int bin) {
       if (bin > wbin) out.put(pos++, key_pos(i), bits);
@@ -737,18 +748,17 @@ cudaError_t launch_select_paged(const PagedCache& c, const PagedLists& lists, cu
   const int rows = c.B * c.Hkv;
   const bool vec = c.page_size % 8 == 0;
   // few rows: as many CTAs per row as the SMs hold at once, each with 4096 keys or
-  // more of the longest row the table can hold (one row of 500k keys: 18 us on
-  // eight CTAs)
+  // more of the longest row the table can hold
   const long long keys = static_cast<long long>(c.max_pages) * c.page_size;
   int csize = 1;
-  while (csize < 8 && 2LL * csize * rows <= nsm && keys >= 4096LL * 2 * csize) csize *= 2;
+  while (csize < kSpMaxCluster && 2LL * csize * rows <= nsm && keys >= 4096LL * 2 * csize) csize *= 2;
   if (csize > 1)
     return vec ? launch_sp<1024, true, true>(c, lists, rows, csize, s)
                : launch_sp<1024, false, true>(c, lists, rows, csize, s);
   // many rows: one CTA each, or as many as give the lists of a large window room
   // while two CTAs share an SM (512 rows of 32k to 64k keys at w = 4000, the step with
   // its attention: 306 us with one CTA an SM, 258 us so)
-  for (; csize < 8; csize *= 2) {
+  for (; csize < kSpMaxCluster; csize *= 2) {
     const Share share = share_of(c, 512 * csize);
     if (share.mean + 2.0 * share.deviation <= most_room<512>(2)) break;
   }
