@@ -142,9 +142,9 @@ __global__ void __launch_bounds__(kPbThreads, kPbMinBlocks)
       issue(slot == 0 ? kPbStages - 1 : slot - 1);   // the step read last time
       slot = slot + 1 == kPbStages ? 0 : slot + 1;
       RowChunk xh = widen_row(xc);
-      // (a row that is not there adds nothing, whatever eps makes of its zeros)
-      const float ms = row_sum<LPR>(chunk_dot(xh, xh)) * (1.0f / D) + a.eps;
-      const float r = act ? rsqrtf(ms) : 0.0f;
+      // (the smallest normal number: a row that is not there is zeros, and adds nothing
+      // with eps = 0 either; asking whether it is there took 1.4 us of 22.5)
+      const float r = rsqrtf(fmaxf(row_sum<LPR>(chunk_dot(xh, xh)) * (1.0f / D) + a.eps, 1.17549435e-38f));
       const unsigned long long r2 = f32x2(r, r);
       RowChunk u = rotate_row_back(widen_row(gc), ang);
 #pragma unroll
