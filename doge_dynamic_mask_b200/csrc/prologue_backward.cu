@@ -26,9 +26,11 @@
 // blocks), so the result does not depend on timing; the last block to finish adds
 // the blocks' shares, so there is no second launch.
 //
-// Measured.  32768 tokens, 16 + 8 heads of 128: 116 us for 604 MB, 5.2 TB/s (94 us
-// at the copy rate).  16384 tokens, 8 + 4 heads of 64: 23 us for 75 MB, of which some
-// 6 us are the start and the join of the weight gradients (74 tokens take 6.1 us).
+// Measured.  32768 tokens, 16 + 8 heads of 128: 115 us for 604 MB, 5.2 TB/s (94 us
+// at the copy rate).  16384 tokens, 8 + 4 heads of 64: 22 us for 75 MB, of which some
+// 6 us are the start and the join of the weight gradients (74 tokens take 5.6 us).
+// Half of the issue slots are used, by four warps a scheduler, which 128 registers a
+// thread allow; ten warps a block in 96 registers spilled: 165 us and 32 us.
 #include <algorithm>
 
 #include "rope.cuh"

@@ -414,6 +414,8 @@ def dma_decode_paged(q, k_pages, v_pages, dt_pages, page_table, lengths, keep_wi
     if dev < 0 or stream is not None or dev != _current_device():
         return _elsewhere(dma_decode_paged, q.device, stream, q, k_pages, v_pages, dt_pages, page_table, lengths,
                           keep_window_size, window, sinks, scale, out, workspace)
+    if (keep_window_size | window | sinks) >> 31 > 0:
+        raise ValueError("keep_window_size, window and sinks must fit 32 bits")
     B, Hq, d = q.shape
     N, page_size, Hkv, _ = k_pages.shape
     max_pages = page_table.shape[1]

@@ -547,6 +547,38 @@ def test_decode_offsets_past_32_bits(dma):
         assert torch.equal(v[int(table[0, j // page]), j % page].cpu(), a["v"][t])
 
 
+def test_binding_names_what_is_wrong(dma):
+    """Arguments that do not fit are refused with their name before anything is launched."""
+    x = append_inputs([3], [0], 4, 2, 64, 8)
+    g = on_gpu(x)
+    q_out = torch.full((3, 4, 64), 77.0, dtype=torch.bfloat16, device="cuda")
+    names = ["q", "k", "v", "q_w", "k_w", "W", "A", "cu", "positions", "table", "k_pages", "v_pages", "dt_pages"]
+    wrong = {"k": g["k"].float(), "v": g["v"][:2], "q_w": g["q_w"][:32], "W": g["W"].T, "A": g["A"].double(),
+             "cu": g["cu"].long(), "positions": torch.cat([g["positions"]] * 2), "table": g["table"].long(),
+             "k_pages": g["k_pages"].transpose(1, 2), "v_pages": g["v_pages"].half(), "dt_pages": g["dt_pages"].transpose(1, 2),
+             "q": g["q"].transpose(1, 2)}
+    for name, t in wrong.items():
+        with pytest.raises(ValueError):
+            dma.dma_append_paged(*[t if n == name else g[n] for n in names], q_out=q_out)
+    with pytest.raises(ValueError, match="workspace|must be"):
+        dma.dma_append_paged(*[g[n] for n in names], q_out=q_out, workspace=torch.zeros(256, dtype=torch.uint8))
+    with pytest.raises(dma.DMAError, match="WORKSPACE"):
+        dma.dma_append_paged(*[g[n] for n in names], q_out=q_out, workspace=dma.new_workspace(128))
+    assert (q_out == 77.0).all()
+    y = decode_inputs([40], 4, 2, 64, 16, garbage=False)
+    h = decode_gpu(y)
+    call = lambda w=2048, **kw: dma.dma_decode_paged(h["q"], kw.pop("k", h["k"]), h["v"], h["dt"], kw.pop("table", h["table"]),
+                                                     h["lens"], w, **kw)
+    for bad in (dict(w=2 ** 32 + 5), dict(window=2 ** 32 + 5), dict(sinks=2 ** 33), dict(k=h["k"][:, :8]),
+                dict(table=h["table"].long()), dict(out=torch.zeros((1, 4, 64), device="cuda"))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    for bad in (dict(window=-1), dict(sinks=-1), dict(scale=float("nan")), dict(scale=1e300)):
+        with pytest.raises((ValueError, dma.DMAError)):
+            call(**bad)
+    check_decode(y, call(), 2048, 0, 0)
+
+
 # ---- streams, graphs, the run together -------------------------------------------------
 
 def test_decode_in_a_graph_follows_its_inputs(dma):
