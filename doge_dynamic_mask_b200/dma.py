@@ -360,7 +360,7 @@ def dma_append_paged(q, k, v, q_norm_w, k_norm_w, W_dt, A, cu_tokens, positions,
     B, max_pages = page_table.shape
     bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     if q_out is None:
-        q_out = torch.empty((T, Hq, d), dtype=bf, device=q.device)
+        q_out = torch.empty(T, Hq, d, dtype=bf, device=q.device)
     if workspace is None:
         workspace = new_workspace(256, q.device)
     kv = (T, Hkv, d)
@@ -421,7 +421,7 @@ def dma_decode_paged(q, k_pages, v_pages, dt_pages, page_table, lengths, keep_wi
     max_pages = page_table.shape[1]
     bf, i32 = torch.bfloat16, torch.int32
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=bf, device=q.device)
+        out = torch.empty(B, Hq, d, dtype=bf, device=q.device)
     if workspace is None:
         size = dma_decode_paged_workspace_size(B, max_pages, page_size, Hq, Hkv, d, keep_window_size, window, sinks)
         if size == 0:
@@ -466,11 +466,11 @@ def dma_prologue_backward(q, k, q_norm_w, k_norm_w, positions, dq_out, dk_out, e
     ks = (B, L, Hkv, d)
     bf, f32 = torch.bfloat16, torch.float32
     if dq is None:
-        dq = torch.empty(qs, dtype=bf, device=q.device)
+        dq = torch.empty(B, L, Hq, d, dtype=bf, device=q.device)
     if dk is None:
-        dk = torch.empty(ks, dtype=bf, device=q.device)
+        dk = torch.empty(B, L, Hkv, d, dtype=bf, device=q.device)
     if dq_norm_w is None and dk_norm_w is None:
-        dq_norm_w, dk_norm_w = torch.empty((2, d), dtype=f32, device=q.device).unbind()
+        dq_norm_w, dk_norm_w = torch.empty_like(q_norm_w), torch.empty_like(k_norm_w)
     elif dq_norm_w is None or dk_norm_w is None:
         raise ValueError("dq_norm_w and dk_norm_w: give both or neither")
     if workspace is None:
