@@ -68,10 +68,6 @@ struct RawChunk {
   uint4 lo, hi;
 };
 
-__device__ __forceinline__ RawChunk load_row(const uint16_t* row, int half) {
-  return RawChunk{__ldg(reinterpret_cast<const uint4*>(row)), __ldg(reinterpret_cast<const uint4*>(row + half))};
-}
-
 __device__ __forceinline__ RowChunk widen_row(const RawChunk& r) {
   RowChunk x;
   x.lo[0] = widen_bf16x2(r.lo.x);
