@@ -22,8 +22,8 @@
 // products run on mma.m16n8k16 with the keys (and, for P V, the channels) on the
 // M side and the group's query heads, at most eight, on the N side: no row of a
 // tile is padding, which tcgen05's 128 rows could not offer to one query, and the
-// tensor work stays far below the copy time.  P is split into two bf16 terms, so
-// its rounding (2^-17) does not show in the output.
+// tensor work stays far below the copy time.  P is split into three bf16 terms, its
+// 24 bits exactly.
 //
 // Measured.  Long rows kept whole (8 sequences of 64k to 128k keys, 8 heads of
 // 128) run at the copy rate: 480 us for 3.2 GB, 6.7 TB/s.  Kept lists of 2048 of
@@ -461,9 +461,14 @@ __global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(
     l0 += p00 + p10;
     l1 += p01 + p11;
     const uint32_t h0 = pack_bf16x2(p00, p01), h1 = pack_bf16x2(p10, p11);
-    const uint32_t e0 = pack_bf16x2(p00 - __uint_as_float(h0 << 16), p01 - __uint_as_float(h0 & 0xFFFF0000u));
-    const uint32_t e1 = pack_bf16x2(p10 - __uint_as_float(h1 << 16), p11 - __uint_as_float(h1 & 0xFFFF0000u));
+    // what the first term leaves, and what the second leaves of that: both differences are exact
+    const float q00 = p00 - __uint_as_float(h0 << 16), q01 = p01 - __uint_as_float(h0 & 0xFFFF0000u);
+    const float q10 = p10 - __uint_as_float(h1 << 16), q11 = p11 - __uint_as_float(h1 & 0xFFFF0000u);
+    const uint32_t e0 = pack_bf16x2(q00, q01), e1 = pack_bf16x2(q10, q11);
+    const uint32_t f0 = pack_bf16x2(q00 - __uint_as_float(e0 << 16), q01 - __uint_as_float(e0 & 0xFFFF0000u));
+    const uint32_t f1 = pack_bf16x2(q10 - __uint_as_float(e1 << 16), q11 - __uint_as_float(e1 & 0xFFFF0000u));
     const uint32_t ph0 = transpose8x8(h0), ph1 = transpose8x8(h1), pe0 = transpose8x8(e0), pe1 = transpose8x8(e1);
+    const uint32_t pf0 = transpose8x8(f0), pf1 = transpose8x8(f1);
     const uint32_t sv = st + Cfg::kTileBytes;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
@@ -471,6 +476,7 @@ __global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(
       ldsm4_t(va, sv + v_row * Cfg::kRowBytes + (((2 * s + v_par) ^ (v_row & 7)) << 4));
       mma16816(o[s], va, ph0, ph1);
       mma16816(o[s], va, pe0, pe1);
+      mma16816(o[s], va, pf0, pf1);
     }
     const int used = slot;
     slot = slot + 1 == STG ? 0 : slot + 1;
