@@ -64,3 +64,42 @@ def test_probabilities_hold_what_bf16_terms_leave(dma, Hq, Hkv, d, w):
     assert (np.abs(want) >= 1.0e-6).all()
     err = np.abs(out.double().cpu().numpy() - want)
     assert (err <= 2.0 ** -8 * np.abs(want) + 3e-7).all(), f"off by {err.max():.2e} of {np.abs(want).min():.2e}"
+
+
+@pytest.mark.parametrize("d,warps", [(64, 16), (128, 8)])
+def test_long_sums_are_rounded_to_nearest(dma, d, warps):
+    """128 rows of 65536 keys: values of 1 and, in three keys at the end, what makes the 64-bit output vanish.  All a
+    warp's sums grow one way, so an addition that cuts off bits (as a chain of tensor-core products does) is off by
+    2^-24 of the sum on average each time, and the output by 1e-5 and more.
+
+    Tolerance, relative to the sum of the probabilities: every tile's sum enters a warp's by one addition, off by at
+    most half an ulp either way: 4 sqrt(tiles) ulps with a probability of 2 e^-32 to be off by more (Hoeffding).  A
+    probability: 2^-22 (2^x) and 1.3e-7 (its score), for the keys and for the last three.  The last tile's three products:
+    2^-23 each.  Joining: an addition of 2^-24 per warp of the row, and 2^-22 of a piece's weight."""
+    page, pages, n, B, Hkv = 64, 9, 65536, 64, 2
+    gen = torch.Generator().manual_seed(d)
+    dt = 0.2 + 0.8 * torch.rand((pages, page), generator=gen)
+    dt[-1, -3:] = 0.7
+    table = torch.randint(0, pages - 1, (n // page,), generator=gen)
+    table[-1] = pages - 1
+    p = torch.exp(dt.double() - 1)[table].flatten()
+    v = torch.ones((pages, page), dtype=torch.float64)
+    rest = -p[:-3].sum()
+    for i in (-3, -2, -1):
+        v[-1, i] = (rest / p[-1]).to(torch.bfloat16).double()
+        rest -= v[-1, i] * p[-1]
+    assert abs(rest) < 1e-7 * p.sum()
+    vp = v.to(torch.bfloat16)[:, :, None, None].expand(pages, page, Hkv, d).contiguous().cuda()
+    kp = torch.randn((pages, page, Hkv, d), generator=gen).to(torch.bfloat16).cuda()
+    dtp = dt[:, None].expand(pages, Hkv, page).contiguous().cuda()
+    q = torch.zeros((B, 2 * Hkv, d), dtype=torch.bfloat16, device="cuda")
+    tab = table.to(torch.int32)[None].expand(B, -1).contiguous().cuda()
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    out = dma.dma_decode_paged(q, kp, vp, dtp, tab, lens, 1 << 20).double().abs().max().item()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    per_warp = -(-B * Hkv * (n // 16) // (sms * warps))
+    ulp = 2.0 ** (np.floor(np.log2(16.0 * per_warp)) - 23)
+    total = p.sum().item()
+    tol = (4 * np.sqrt(n // 16) * ulp / total + 2 * (2.0 ** -22 + 1.3e-7) + 3 * 2.0 ** -23
+           + (n // 16 // per_warp + 2) * 2.0 ** -24 + 2.0 ** -22)
+    assert tol < 8e-6 and out <= tol, f"{out:.2e}, tolerance {tol:.2e}"
