@@ -58,7 +58,8 @@ struct PbArgs {
   RowShare share;
 };
 
-template <int D>
+// EPS: eps > 0
+template <int D, bool EPS>
 __global__ void __launch_bounds__(kPbThreads, kPbMinBlocks)
     prologue_bwd_kernel(const __grid_constant__ PbArgs a, const __grid_constant__ RopeTurns turns) {
   constexpr int LPR = D / 16;          // lanes per row
@@ -144,9 +145,10 @@ __global__ void __launch_bounds__(kPbThreads, kPbMinBlocks)
       issue(slot == 0 ? kPbStages - 1 : slot - 1);   // the step read last time
       slot = slot + 1 == kPbStages ? 0 : slot + 1;
       RowChunk xh = widen_row(xc);
-      // (the smallest normal number: a row that is not there is zeros, and adds nothing
-      // with eps = 0 either; asking whether it is there took 1.4 us of 22.5)
-      const float r = rsqrtf(fmaxf(row_sum<LPR>(chunk_dot(xh, xh)) * (1.0f / D) + a.eps, 1.17549435e-38f));
+      // a row that is not there is zeros: its r is finite and it adds nothing, unless eps is 0
+      // (kernels of their own: asking takes 1.4 us of 22.5)
+      float r = rsqrtf(row_sum<LPR>(chunk_dot(xh, xh)) * (1.0f / D) + a.eps);
+      if (!EPS && !act) r = 0.0f;
       const unsigned long long r2 = f32x2(r, r);
       RowChunk u = rotate_row_back(widen_row(gc), ang);
 #pragma unroll
@@ -278,7 +280,8 @@ cudaError_t launch_prologue_backward(const PrologueBackward& p, cudaStream_t s) 
   // a warp per item: few blocks, and few shares to add, when there are few items (74
   // tokens: 5.7 us, with a block in every slot 7.6 us)
   const int blocks = std::min((a.share.items + kPbWarps - 1) / kPbWarps, slots);
-  auto* kernel = p.d == 64 ? prologue_bwd_kernel<64> : prologue_bwd_kernel<128>;
+  auto* kernel = p.d == 64 ? (p.eps > 0.0f ? prologue_bwd_kernel<64, true> : prologue_bwd_kernel<64, false>)
+                           : (p.eps > 0.0f ? prologue_bwd_kernel<128, true> : prologue_bwd_kernel<128, false>);
   const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), kPbSmemBytes);
   if (e != cudaSuccess) return e;
   return launch_after(kernel, dim3(blocks), dim3(kPbThreads), kPbSmemBytes, s, a, turns);
