@@ -120,14 +120,6 @@ struct RowAngles {
   unsigned long long cs[4], sn[4];
 };
 
-// The reduced angle lies in [-pi, pi], where the fast sine and cosine are off by
-// at most 2^-21 of the channels they multiply: a thousandth of the bf16 rounding
-// that follows, for a tenth of the instructions.
-__device__ __forceinline__ void rope_cos_sin_fast(double pos, double turn, float& cs, float& sn) {
-  const double u = pos * turn;
-  __sincosf(6.28318531f * static_cast<float>(u - rint(u)), &sn, &cs);
-}
-
 // How a grid's warps share the head rows of q and of k.  A warp step takes 128 /
 // d tokens and four consecutive heads of each, so a token's step is 4 d
 // contiguous channels; a token has ceil(Hq / 4) steps in q, then ceil(Hkv / 4) in
@@ -189,7 +181,7 @@ __device__ __forceinline__ RowAngles token_angles(double pos, const double* turn
   const int lane = threadIdx.x & 31, l = lane % LPR;
   float c[2], s[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) rope_cos_sin_fast(pos, turns[2 * (lane % UL) + i], c[i], s[i]);
+  for (int i = 0; i < 2; ++i) rope_cos_sin(pos, turns[2 * (lane % UL) + i], c[i], s[i]);
   RowAngles a;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {   // angles 8 l + 2 e and the next sit in lane 4 l + e

@@ -115,3 +115,23 @@ def test_a_row_of_zeros_has_no_gradient_without_eps(dma, B, L, Hq, Hkv, d):
     tiny = run(dma, x, 1e-45)
     assert tiny["k_w"].isfinite().all() and tiny["k"].isfinite().all()
     assert torch.equal(tiny["k"][~row], got["k"][~row]) and torch.equal(tiny["q_w"], got["q_w"])
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 4, 64), (2, 1, 128)])
+def test_small_angles_reach_the_weights(dma, Hq, Hkv, d):
+    """A gradient of the upper channels only: dw of a lower channel is sum_h g sin(a) x r, all terms positive, so it is
+    exact to a few roundings of itself: g sin(a) and its angle 2^-23 each (the angle is below 1, so a relative error of
+    it is one of its sine), sin 2^-23, x r 2^-21.5 (the inverse root 2^-22.5, its argument's some ten roundings of
+    2^-24, halved), the sum over heads 2^-22: 2^-20 in all.  dw of an upper channel has cos(a) in place of the sine."""
+    x = inputs(1, 1, Hq, Hkv, d, seed=d)
+    x["positions"] = torch.tensor([1], dtype=torch.int32)
+    for n in ("q", "k", "dq_out", "dk_out"):
+        x[n] = (x[n].float().abs() + 0.5).to(torch.bfloat16)
+    for n in ("dq_out", "dk_out"):
+        x[n][..., :d // 2] = 0
+    got = run(dma, x)
+    want = oracle.prologue_backward(f64(x["q"]), f64(x["k"]), f64(x["q_w"]), f64(x["k_w"]), 1e-6, 10000.0, [1],
+                                    f64(x["dq_out"]), f64(x["dk_out"]))
+    for n, dw in (("q_w", want[2]), ("k_w", want[3])):
+        err = np.abs(f64(got[n]) - dw) / np.abs(dw)
+        assert (err <= 2.0 ** -20).all(), f"{n}: {err.max():.2e}"
