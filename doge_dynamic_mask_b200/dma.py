@@ -401,6 +401,8 @@ def dma_append_paged(q, k, v, q_norm_w, k_norm_w, W_dt, A, cu_tokens, positions,
 
 
 def dma_decode_paged_workspace_size(B, max_pages, page_size, Hq, Hkv, d, keep_window_size, window=0, sinks=0) -> int:
+    if (B | max_pages | page_size | Hq | Hkv | d | keep_window_size | window | sinks) >> 31:
+        return 0   # ctypes would take them modulo 2^32
     return int(_lib.dma_decode_paged_workspace_size(B, max_pages, page_size, Hq, Hkv, d, keep_window_size, window,
                                                     sinks))
 
@@ -410,12 +412,12 @@ def dma_decode_paged(q, k_pages, v_pages, dt_pages, page_table, lengths, keep_wi
     """One new query per sequence ([B, Hq, d]) over a paged cache: of the keys a sequence of lengths[b] tokens
     sees (all, or the last `window` and the first `sinks`) the keep_window_size best by dt_pages, with dt as an
     additive bias.  A length of 0 gives a zero row."""
+    if (keep_window_size | window | sinks) >> 31:
+        raise ValueError("keep_window_size, window and sinks must lie in [0, 2^31)")
     dev = q.get_device()
     if dev < 0 or stream is not None or dev != _current_device():
         return _elsewhere(dma_decode_paged, q.device, stream, q, k_pages, v_pages, dt_pages, page_table, lengths,
                           keep_window_size, window, sinks, scale, out, workspace)
-    if (keep_window_size | window | sinks) >> 31 > 0:
-        raise ValueError("keep_window_size, window and sinks must fit 32 bits")
     B, Hq, d = q.shape
     N, page_size, Hkv, _ = k_pages.shape
     max_pages = page_table.shape[1]
@@ -450,6 +452,8 @@ def dma_decode_paged(q, k_pages, v_pages, dt_pages, page_table, lengths, keep_wi
 
 
 def dma_prologue_backward_workspace_size(B, L, Hq, Hkv, d) -> int:
+    if (B | L | Hq | Hkv | d) >> 31:
+        return 0   # ctypes would take them modulo 2^32
     return int(_lib.dma_prologue_backward_workspace_size(B, L, Hq, Hkv, d))
 
 
