@@ -8,6 +8,7 @@
 
 #include "../../include/dma.h"
 #include "dma_internal.h"
+#include "smem_limits.h"
 
 namespace dma {
 
@@ -94,26 +95,13 @@ int sm_count() {
 }
 
 cudaError_t ensure_dyn_smem(const void* func, int bytes) {
-  struct Entry {
-    const void* func;
-    int dev, bytes;
-  };
-  static std::mutex mu;
-  static Entry table[64];
-  static int n = 0;
+  static SmemLimits limits;
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  int slot = -1;
-  for (int i = 0; i < n; ++i)
-    if (table[i].func == func && table[i].dev == dev) slot = i;
-  if (slot >= 0 && table[slot].bytes >= bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  if (slot < 0 && n < 64) slot = n++;
-  if (slot >= 0) table[slot] = Entry{func, dev, bytes};
-  return cudaSuccess;
+  return static_cast<cudaError_t>(limits.raise(func, dev, bytes, [&] {
+    return static_cast<int>(cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  }));
 }
 
 size_t prefill_plan_bytes(const Geometry& g) {
