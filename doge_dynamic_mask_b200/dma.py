@@ -119,6 +119,13 @@ def new_workspace(nbytes: int, device=None) -> torch.Tensor:
     return torch.zeros(int(nbytes), dtype=torch.uint8, device=device or "cuda")
 
 
+def _scratch(nbytes: int, device) -> torch.Tensor:
+    """A workspace of which only the header is zeroed, for the calls that need no more."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
 def dma_dt_scores(v, W_dt, A, dt_out=None, stream=None):
     B, L, Hkv, d = v.shape
     if dt_out is None:
@@ -428,7 +435,7 @@ def dma_decode_paged(q, k_pages, v_pages, dt_pages, page_table, lengths, keep_wi
         size = dma_decode_paged_workspace_size(B, max_pages, page_size, Hq, Hkv, d, keep_window_size, window, sinks)
         if size == 0:
             raise ValueError("unsupported paged decode geometry")
-        workspace = new_workspace(size, q.device)
+        workspace = _scratch(size, q.device)
     if not (q.dtype is bf and k_pages.dtype is bf and v_pages.dtype is bf and out.dtype is bf
             and dt_pages.dtype is torch.float32 and page_table.dtype is i32 and lengths.dtype is i32
             and out.shape == (B, Hq, d) and k_pages.shape[3] == d and dt_pages.shape == (N, Hkv, page_size)
@@ -481,7 +488,7 @@ def dma_prologue_backward(q, k, q_norm_w, k_norm_w, positions, dq_out, dk_out, e
         size = dma_prologue_backward_workspace_size(B, L, Hq, Hkv, d)
         if size == 0:
             raise ValueError("unsupported prologue geometry")
-        workspace = new_workspace(size, q.device)
+        workspace = _scratch(size, q.device)
     if not (q.dtype is bf and k.dtype is bf and dq_out.dtype is bf and dk_out.dtype is bf and dq.dtype is bf
             and dk.dtype is bf and q_norm_w.dtype is f32 and k_norm_w.dtype is f32 and dq_norm_w.dtype is f32
             and dk_norm_w.dtype is f32 and positions.dtype is torch.int32

@@ -1,0 +1,72 @@
+"""Workspaces that the binding makes for a call: only their header is zeroed, and nothing else is needed."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dma():
+    from doge_dynamic_mask_b200 import build
+    build.build()
+    from doge_dynamic_mask_b200 import dma as m
+    return m
+
+
+def marked(size):
+    """Leaves a block of `size` bytes of 0xA5 to the allocator; returns its address."""
+    t = torch.full((size,), 0xA5, dtype=torch.uint8, device="cuda")
+    at = t.data_ptr()
+    torch.cuda.synchronize()
+    del t
+    return at
+
+
+def what_is_left(size, at):
+    t = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert t.data_ptr() == at, "the allocator gave another block: nothing to see here"
+    return t
+
+
+@pytest.mark.parametrize("w", [40, 2048])
+def test_decode_without_a_workspace_zeroes_the_header_alone(dma, w):
+    B, Hq, Hkv, d, page, pages = 3, 16, 2, 128, 16, 8
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda").to(torch.bfloat16)
+    q, k, v = rand(B, Hq, d), rand(B * pages, page, Hkv, d), rand(B * pages, page, Hkv, d)
+    dt = torch.rand((B * pages, Hkv, page), generator=gen, device="cuda")
+    table = torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages)
+    lens = torch.tensor([100, 0, 127], dtype=torch.int32, device="cuda")
+    size = dma.dma_decode_paged_workspace_size(B, pages, page, Hq, Hkv, d, w)
+    ws, out, want = dma.new_workspace(size), torch.empty_like(q), torch.empty_like(q)
+    dma.dma_decode_paged(q, k, v, dt, table, lens, w, out=want, workspace=ws)
+    del ws
+    torch.cuda.empty_cache()
+    at = marked(size)
+    dma.dma_decode_paged(q, k, v, dt, table, lens, w, out=out)
+    assert torch.equal(out, want)
+    t = what_is_left(size, at)
+    assert not t[:256].any()
+    assert (t[256:] == 0xA5).float().mean() > 0.5
+
+
+def test_prologue_backward_without_a_workspace_zeroes_the_header_alone(dma):
+    B, L, Hq, Hkv, d = 2, 37, 8, 4, 128
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda").to(torch.bfloat16)
+    q, k, gq, gk, dq, dk = (rand(B, L, h, d) for h in (Hq, Hkv) * 3)
+    one, pos = torch.ones(d, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    dw = [torch.empty_like(one) for _ in range(4)]
+    call = lambda a, b, ws=None: dma.dma_prologue_backward(q, k, one, one, pos, gq, gk, dq=dq, dk=dk, dq_norm_w=a,
+                                                           dk_norm_w=b, workspace=ws)
+    size = dma.dma_prologue_backward_workspace_size(B, L, Hq, Hkv, d)
+    ws = dma.new_workspace(size)
+    call(*dw[:2], ws)
+    del ws
+    torch.cuda.empty_cache()
+    at = marked(size)
+    call(*dw[2:])
+    assert torch.equal(dw[0], dw[2]) and torch.equal(dw[1], dw[3])
+    t = what_is_left(size, at)
+    assert not t[:256].any()
+    assert (t[256:] == 0xA5).float().mean() > 0.5
