@@ -542,14 +542,14 @@ def decode_state_views(state, B, Lk, Hq, Hkv, d, keep_window_size):
 def paged_list_views(workspace, B, Hq, Hkv, d, keep_window_size):
     """(positions [B, Hkv, w] int32, bias [B, Hkv, w] float32) of a paged decode workspace with kept lists, for tests:
     a kept key's position in its sequence (-1: no key), and its dt.  Written for the rows that see more than w keys.
-    The scratch of 160 blocks of sixteen warps lies before them."""
-    def up(x):
-        return -(-x // 256) * 256
+    They are the workspace's last two parts, each rounded up to 256 bytes; what lies before them depends on the head
+    shapes alone, so the size for the shortest table with lists tells where they begin."""
     n = B * Hkv * keep_window_size * 4
-    off = up(256 + 160 * 17 * 2 * (Hq // Hkv) * (d + 8) * 4)
+    part = -(-n // 256) * 256
+    bias = dma_decode_paged_workspace_size(B, keep_window_size + 1, 1, Hq, Hkv, d, keep_window_size) - part
     shape = (B, Hkv, keep_window_size)
-    return (workspace[off:off + n].view(torch.int32).view(shape),
-            workspace[up(off + n):up(off + n) + n].view(torch.float32).view(shape))
+    return (workspace[bias - part:bias - part + n].view(torch.int32).view(shape),
+            workspace[bias:bias + n].view(torch.float32).view(shape))
 
 
 def dma_selftest_wait(workspace, stream=None):

@@ -37,3 +37,19 @@ def test_workspace_sizes_are_zero_beyond_32_bits(dma, bad):
     assert dma.dma_prologue_backward_workspace_size(**backward) > 0
     for name in backward:
         assert dma.dma_prologue_backward_workspace_size(**dict(backward, **{name: bad})) == 0, name
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,w", [(8, 4, 64, 100), (16, 2, 128, 2048), (3, 1, 128, 1), (16, 16, 64, 33)])
+def test_list_views_are_the_last_parts_of_the_workspace(dma, Hq, Hkv, d, w):
+    """Whatever lies before them: both lists, each rounded up to 256 bytes, end the workspace of every table."""
+    B = 3
+    n, up = B * Hkv * w * 4, lambda x: -(-x // 256) * 256
+    for max_pages, page in ((w + 1, 1), (500, 16), (7000, 100)):
+        size = dma.dma_decode_paged_workspace_size(B, max_pages, page, Hq, Hkv, d, w)
+        ws = torch.zeros(size, dtype=torch.uint8)
+        pos, bias = dma.paged_list_views(ws, B, Hq, Hkv, d, w)
+        assert pos.dtype == torch.int32 and bias.dtype == torch.float32 and pos.shape == bias.shape == (B, Hkv, w)
+        at = [t.data_ptr() - ws.data_ptr() for t in (pos, bias)]
+        assert at == [size - 2 * up(n), size - up(n)]
+    # without lists the workspace is that much smaller
+    assert dma.dma_decode_paged_workspace_size(B, w, 1, Hq, Hkv, d, w) == size - 2 * up(n)
