@@ -224,6 +224,13 @@ __device__ __forceinline__ int bin_shift(uint32_t range) {
   return top > 11 ? top - 11 : 0;
 }
 
+// The highest value of the bin that begins at lo, or hi where that is lower (without
+// the sum's overflow: bits near 2^32, which no dt >= 0 has, must not widen the range
+// or leave it empty).
+__device__ __forceinline__ uint32_t bin_top(uint32_t lo, int shift, uint32_t hi) {
+  return hi - lo < (1u << shift) ? hi : lo + ((1u << shift) - 1u);
+}
+
 // Sum of the warps' values before this warp, from one value per warp.
 __device__ __forceinline__ uint32_t warps_before(const uint32_t* per_warp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -352,7 +359,7 @@ static __device__ __noinline__ void select_exact(const PagedCache& c, const Kept
       uint32_t bin, cnt;
       top_bin<THREADS>(sm, k, NoOthers{}, bin, k, cnt);
       const uint32_t l2 = lo + (bin << s);
-      hi = min(hi, l2 + ((1u << s) - 1u));
+      hi = bin_top(l2, s, hi);
       lo = l2;
     }
   } else {
@@ -475,7 +482,7 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
       uint32_t bin, cnt;
       top_bin<THREADS>(sm, k, NoOthers{}, bin, k, cnt);
       const uint32_t l2 = lo + (bin << s);
-      hi = min(hi, l2 + ((1u << s) - 1u));
+      hi = bin_top(l2, s, hi);
       lo = l2;
       if (cnt <= 16u) break;   // its lower edge takes a few more keys than the exact value would
       tied = lo == hi;
@@ -483,10 +490,10 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
     thr = lo;
   }
   const uint32_t tie = thr;
-  if (tied || thr == 0u) {   // (0: positions that are not seen read as 0, below every threshold)
-    tied = true;
-    ++thr;
-  }
+  // (0: positions that are not seen read as 0, below every threshold; nothing lies above
+  // 2^32 - 1, whose row comes out right by collecting the tied keys themselves)
+  tied = (tied || thr == 0u) && thr != 0xFFFFFFFFu;
+  if (tied) ++thr;
   __syncthreads();   // the sample has been read: keys are written over it
 
   // ---- collect, an oct per thread and step
