@@ -138,7 +138,6 @@ struct KeyPage {
 
 // What a warp leaves of a row that its range cuts: slot 0 a row that began
 // before the range, slot 1 one that begins in it and goes on.
-enum : int { kNone = 0, kEnds = 1, kThrough = 2, kOpen = 3 };
 struct RowCut {
   uint32_t t0;       // the row's first tile on the axis
   int nt, b, g;
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(
   constexpr int STG = Cfg::kStages;
   extern __shared__ __align__(128) unsigned char ring_all[];
   __shared__ RowCut s_cut[kDpWarps][2];
-  __shared__ int s_kind[kDpWarps][2];
+  __shared__ bool s_left[kDpWarps][2];   // the warp left such a piece
   __shared__ int s_last[2];
   const PagedCache& c = a.c;
   pdl_wait();
@@ -299,7 +298,7 @@ __global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(
     cur.g = static_cast<int>(rem / static_cast<uint32_t>(cur.nt));
     cur.t = static_cast<int>(rem) - cur.g * cur.nt;
   }
-  if (lane < 2) s_kind[warp][lane] = kNone;
+  if (lane < 2) s_left[warp][lane] = false;
   if (tid < 2) s_last[tid] = 0;
   const int nrep = a.Hq / c.Hkv;
   constexpr int PF = piece_floats(D);
@@ -529,7 +528,7 @@ __global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(
         if (gid == 0 && ha < nrep) write_ml(dst + ha * PF + D, m0, L0);
         if (gid == 0 && hb < nrep) write_ml(dst + hb * PF + D, m1, L1);
         if (lane == 0) {
-          s_kind[warp][cut] = cut ? kOpen : (row_end ? kEnds : kThrough);
+          s_left[warp][cut] = true;
           s_cut[warp][cut] = RowCut{x0 + static_cast<uint32_t>(x) - static_cast<uint32_t>(cur.t), cur.nt, cur.b, cur.g};
         }
       }
@@ -553,7 +552,7 @@ __global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(
   RowCut cut{};
   int w0 = 0, w1 = 0;      // the chain's warps
   bool right = false;      // it goes on past the block
-  const bool mine = lane < kDpWarps ? s_kind[lane][1] == kOpen : lane == kDpWarps && s_kind[first][0] != kNone;
+  const bool mine = lane < kDpWarps ? s_left[lane][1] : lane == kDpWarps && s_left[first][0];
   if (mine) {
     w0 = lane < kDpWarps ? lane : first;
     cut = s_cut[w0][lane < kDpWarps ? 1 : 0];

@@ -187,8 +187,9 @@ cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t s
 
 // Entry-point helpers shared by the C ABI's translation units: record a CUDA
 // error for dma_last_cuda_error() and return DMA_ERR_CUDA; the sm_100 device
-// check; the head shapes every entry point supports; and the argument checks of dma_decode_step (everything it verifies
-// before it enqueues work, workspace size aside).
+// check; the head shapes every entry point supports; and the argument checks of
+// dma_decode_step (everything it verifies before it enqueues work, workspace size
+// aside).
 dma_status_t cuda_fail(cudaError_t e);
 dma_status_t device_ok();
 dma_status_t check_heads(int Hq, int Hkv, int d);
@@ -219,7 +220,7 @@ cudaError_t launch_prologue(const void* q, const void* k, const void* v, const f
                             float eps, float theta, const int32_t* positions, int B, int L, int Lmax, int Hq, int Hkv,
                             int d, void* q_out, void* k_cache, void* v_cache, uint32_t* err, cudaStream_t s);
 // paged cache: append, selection of the rows longer than the kept window, attention
-// (scratch: attn_paged_scratch_bytes, zeroed before its first use)
+// (scratch: attn_paged_scratch_bytes, which may hold anything; the header's counters are zero)
 cudaError_t launch_append_paged(const AppendPaged& p, uint32_t* err, cudaStream_t s);
 cudaError_t launch_select_paged(const PagedCache& c, const PagedLists& lists, cudaStream_t s);
 cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, const void* q, const void* k_pages,
