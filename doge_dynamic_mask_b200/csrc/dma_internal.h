@@ -100,6 +100,7 @@ struct PagedCache {
   int page_shift;                 // log2(page_size), or -1
   float page_inv;                 // 1 / page_size
   int Hkv, d, w, window, sinks;   // window 0: every key below the length is visible
+  int longest;                    // keys of the longest row a query can see: the table's, or the window's and the sinks'
   uint32_t* err;
 };
 

@@ -141,6 +141,7 @@ dma_status_t dma_decode_paged(const void* q, const void* k_pages, const void* v_
   c.w = keep_window_size;
   c.window = std::min(window, kMaxLen);   // a longer one reaches every key, like kMaxLen
   c.sinks = window > 0 ? std::min(sinks, kMaxLen) : 0;
+  c.longest = static_cast<int>(visible_cap(max_pages, page_size, window, sinks));
   c.err = reinterpret_cast<uint32_t*>(ws);
   PagedLists lists{nullptr, nullptr, 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -699,15 +699,15 @@ __global__ void __launch_bounds__(THREADS, SpCfg<THREADS>::kMinBlocks)
   if (bad && rank == 0) select_exact<THREADS, VEC>(c, out, r, w, sm);
 }
 
-// List entries per thread in the longest row the table can hold, over `threads`
-// threads: the share of the keys expected above the threshold, and its standard
-// deviation (of the threshold's rank in the sample, and of the share).
+// List entries per thread in the longest row, over `threads` threads: the share of the
+// keys expected above the threshold, and its standard deviation (of the threshold's
+// rank in the sample, and of the share).
 struct Share {
   double mean, deviation;
 };
 
 Share share_of(const PagedCache& c, int threads) {
-  const double keys = static_cast<double>(c.max_pages) * c.page_size;
+  const double keys = static_cast<double>(c.longest);
   const double ratio = keys / (keys > kSpSampleLong ? 8.0 * kSpSample : 4.0 * kSpSample);   // keys per sampled one
   const double rank = sample_rank(c.w / ratio);
   const double mean = rank * ratio / threads;
@@ -756,11 +756,12 @@ cudaError_t launch_select_paged(const PagedCache& c, const PagedLists& lists, cu
   const int rows = c.B * c.Hkv;
   const bool vec = c.page_size % 8 == 0;
   // few rows: as many CTAs per row as the SMs hold at once, each with 4096 keys or
-  // more of the longest row the table can hold (one sequence of 500k keys, 8 heads,
-  // attention included: 28.5 us on eight CTAs a row, 109 us on one)
-  const long long keys = static_cast<long long>(c.max_pages) * c.page_size;
+  // more of the longest row (one sequence of 500k keys, 8 heads,
+  // attention included: 28.5 us on eight CTAs a row, 109 us on one; 4 rows of a window of
+  // 8196 keys on 4 heads in tables of 500k: 19.8 us on two CTAs a row, 33.2 us on the eight
+  // that the tables' length would ask for)
   int csize = 1;
-  while (csize < kSpMaxCluster && 2LL * csize * rows <= nsm && keys >= 4096LL * 2 * csize) csize *= 2;
+  while (csize < kSpMaxCluster && 2LL * csize * rows <= nsm && c.longest >= 4096 * 2 * csize) csize *= 2;
   if (csize > 1)
     return vec ? launch_sp<1024, true, true>(c, lists, rows, csize, s)
                : launch_sp<1024, false, true>(c, lists, rows, csize, s);
