@@ -42,6 +42,7 @@ constexpr int kDpMaxWarps = 16;
 constexpr int kTileKeys = 16;
 constexpr uint32_t kRowSteps = 3;   // tiles of a warp that cost less than joining a row's blocks
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kFewWarpsLength = 4096;   // longest row (d = 64) for which blocks of eight warps are taken
 
 // W: warps of a block.  d = 128 takes 204 registers a thread: eight, 25 KB of ring
 // each.  d = 64 has room for sixteen (see the launch).
@@ -667,9 +668,10 @@ cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, cons
   // d = 64: sixteen warps keep more scattered rows on their way (64 sequences with
   // lists of 2048 on 8 heads, selection included: 116 us, eight warps 139 us; 16 of 500
   // to 700 keys on 4 heads: 9.5 and 10.3 us); eight start and join sooner, which counts
-  // while there are few rows (one sequence of 301 keys: 7.4 and 6.5 us; of 2048: 9.5 and
-  // 8.5 us; 8 of 100 to 400: 8.1 and 7.8 us)
-  const bool few = lists.cap == 0 && 4 * c.B * c.Hkv <= nsm;
+  // while there are few and short rows (one sequence of 301 keys, 4 heads: 7.6 and 7.0 us;
+  // of 2048: 9.6 and 8.9 us; of 4096: 10.2 and 10.0 us; of 32k: 16.9 and 17.4 us; of 512k: 94
+  // and 113 us; two of 301 keys: 7.7 and 7.1 us, of 131k: 54 and 62 us)
+  const bool few = lists.cap == 0 && 4 * c.B * c.Hkv <= nsm && c.longest <= kFewWarpsLength;
   return few ? launch_dp<64, 8>(a, blocks, s) : launch_dp<64, 16>(a, blocks, s);
 }
 
