@@ -23,7 +23,9 @@
 // M side and the group's query heads, at most eight, on the N side: no row of a
 // tile is padding, which tcgen05's 128 rows could not offer to one query, and the
 // tensor work stays far below the copy time.  P is split into three bf16 terms, its
-// 24 bits exactly.
+// 24 bits exactly; groups of one or two heads have the terms side by side in the eight
+// columns (8 sequences of 64k to 128k keys, call after call: 484 us so, 492 us with three
+// products each), and larger groups take three products.
 //
 // Measured.  Long rows kept whole (8 sequences of 64k to 128k keys, 8 heads of
 // 128) run at the copy rate: 480 us for 3.2 GB, 6.7 TB/s.  Kept lists of 2048 of
@@ -98,6 +100,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// the eight leading bits of a value, and those of two as bf16 (a in the low half)
+__device__ __forceinline__ float leading_bits(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_leading(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
 
 __device__ __forceinline__ int row_tiles(int keys) { return max(1, (keys + kTileKeys - 1) / kTileKeys); }
@@ -205,7 +213,11 @@ __device__ __forceinline__ void write_out(uint16_t* out, float den, const float4
       make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
 }
 
-template <int D, int W>
+// PAIR: a group has one or two query heads.  The eight columns of P then hold its three
+// terms at once, term t4 of the two heads in the columns of the quad's lane t4 (every
+// lane of a quad computes the same two heads), and o its three sums, joined at a row's
+// end: one product per 16 channels instead of three.
+template <int D, int W, bool PAIR>
 __global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(const __grid_constant__ DpArgs a) {
   using Cfg = DpCfg<D, W>;
   constexpr int kDpWarps = Cfg::kWarps;
@@ -396,11 +408,12 @@ __global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(
     if (fresh) {
       fresh = false;
       from_start = cur.t == 0;
-      const uint16_t* qr = a.q + (static_cast<size_t>(cur.b) * a.Hq + cur.g * nrep + gid) * D + 2 * t4;
+      const int head = PAIR ? gid & 1 : gid;
+      const uint16_t* qr = a.q + (static_cast<size_t>(cur.b) * a.Hq + cur.g * nrep + head) * D + 2 * t4;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        qf[s][0] = gid < nrep ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * s)) : 0u;
-        qf[s][1] = gid < nrep ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * s + 8)) : 0u;
+        qf[s][0] = head < nrep ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * s)) : 0u;
+        qf[s][1] = head < nrep ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * s + 8)) : 0u;
         o[s][0] = o[s][1] = o[s][2] = o[s][3] = 0.0f;
       }
       m0 = m1 = -INFINITY;
@@ -460,30 +473,53 @@ __global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(
     const float p10 = s10 == -INFINITY ? 0.0f : fast_exp2(s10 - m0), p11 = s11 == -INFINITY ? 0.0f : fast_exp2(s11 - m1);
     l0 += p00 + p10;
     l1 += p01 + p11;
-    const uint32_t h0 = pack_bf16x2(p00, p01), h1 = pack_bf16x2(p10, p11);
-    // what the first term leaves, and what the second leaves of that: both differences are exact
-    const float q00 = p00 - __uint_as_float(h0 << 16), q01 = p01 - __uint_as_float(h0 & 0xFFFF0000u);
-    const float q10 = p10 - __uint_as_float(h1 << 16), q11 = p11 - __uint_as_float(h1 & 0xFFFF0000u);
-    const uint32_t e0 = pack_bf16x2(q00, q01), e1 = pack_bf16x2(q10, q11);
-    const uint32_t f0 = pack_bf16x2(q00 - __uint_as_float(e0 << 16), q01 - __uint_as_float(e0 & 0xFFFF0000u));
-    const uint32_t f1 = pack_bf16x2(q10 - __uint_as_float(e1 << 16), q11 - __uint_as_float(e1 & 0xFFFF0000u));
-    const uint32_t ph0 = transpose8x8(h0), ph1 = transpose8x8(h1), pe0 = transpose8x8(e0), pe1 = transpose8x8(e1);
-    const uint32_t pf0 = transpose8x8(f0), pf1 = transpose8x8(f1);
+    // P in three terms of eight bits: its leading ones, those of what they leave, and the rest
+    // (all differences are exact)
+    const float r00 = p00 - leading_bits(p00), r01 = p01 - leading_bits(p01);
+    const float r10 = p10 - leading_bits(p10), r11 = p11 - leading_bits(p11);
+    const float u00 = r00 - leading_bits(r00), u01 = r01 - leading_bits(r01);
+    const float u10 = r10 - leading_bits(r10), u11 = r11 - leading_bits(r11);
     // A tile's sums start at zero, the smallest terms first, and enter o by an addition
     // that rounds to nearest: the tensor core cuts off what it adds to an accumulator, so a
     // chain over a row's tiles loses 2^-24 of the sum each time, always the same way
     // (131072 keys a row: 5e-6 of an output's terms and more)
     const uint32_t sv = st + Cfg::kTileBytes;
+    constexpr int kAtOnce = 2;   // independent products in a row: none waits for the one before it
+    auto values = [&](auto&& products) {
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      uint32_t va[4];
-      ldsm4_t(va, sv + v_row * Cfg::kRowBytes + (((2 * s + v_par) ^ (v_row & 7)) << 4));
-      float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      mma16816(t, va, pf0, pf1);
-      mma16816(t, va, pe0, pe1);
-      mma16816(t, va, ph0, ph1);
+      for (int s0 = 0; s0 < KS; s0 += kAtOnce) {
+        uint32_t va[kAtOnce][4];
+        float t[kAtOnce][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[s][i] += t[i];
+        for (int s = 0; s < kAtOnce; ++s) {
+          ldsm4_t(va[s], sv + v_row * Cfg::kRowBytes + (((2 * (s0 + s) + v_par) ^ (v_row & 7)) << 4));
+          t[s][0] = t[s][1] = t[s][2] = t[s][3] = 0.0f;
+        }
+        products(t, va);
+#pragma unroll
+        for (int s = 0; s < kAtOnce; ++s)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[s0 + s][i] += t[s][i];
+      }
+    };
+    auto term = [&](float (&t)[kAtOnce][4], const uint32_t (&va)[kAtOnce][4], uint32_t p0, uint32_t p1) {
+#pragma unroll
+      for (int s = 0; s < kAtOnce; ++s) mma16816(t[s], va[s], p0, p1);
+    };
+    if constexpr (PAIR) {
+      auto mine = [&](float p, float r, float u) { return t4 == 0 ? p : t4 == 1 ? r : t4 == 2 ? u : 0.0f; };
+      const uint32_t m0 = transpose8x8(pack_leading(mine(p00, r00, u00), mine(p01, r01, u01)));
+      const uint32_t m1 = transpose8x8(pack_leading(mine(p10, r10, u10), mine(p11, r11, u11)));
+      values([&](auto& t, const auto& va) { term(t, va, m0, m1); });
+    } else {
+      const uint32_t ph0 = transpose8x8(pack_leading(p00, p01)), ph1 = transpose8x8(pack_leading(p10, p11));
+      const uint32_t pe0 = transpose8x8(pack_leading(r00, r01)), pe1 = transpose8x8(pack_leading(r10, r11));
+      const uint32_t pf0 = transpose8x8(pack_leading(u00, u01)), pf1 = transpose8x8(pack_leading(u10, u11));
+      values([&](auto& t, const auto& va) {
+        term(t, va, pf0, pf1);
+        term(t, va, pe0, pe1);
+        term(t, va, ph0, ph1);
+      });
     }
     const int used = slot;
     slot = slot + 1 == STG ? 0 : slot + 1;
@@ -500,32 +536,45 @@ __global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(
       // through the stage just read (its K rows' place), so that rows of o leave in
       // whole 128-byte lines: written from the accumulators as they lie, four bytes a
       // lane, a block's pieces took 1 to 2 us
-      float* turn = reinterpret_cast<float*>(ring + used * Cfg::kStageBytes);   // [head][d]
+      float* turn = reinterpret_cast<float*>(ring + used * Cfg::kStageBytes);   // [head][d]; PAIR: [term][2][d]
+      constexpr int kTerm = 2 * D + 8;   // floats between terms: the quad's lanes write to other banks
+      const bool wa = PAIR ? t4 < 3 : ha < nrep, wb = PAIR ? t4 < 3 && nrep == 2 : hb < nrep;
+      float *ta = turn + (PAIR ? t4 * kTerm : ha * D) + gid, *tb = ta + D;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        if (ha < nrep) {
-          turn[ha * D + 16 * s + gid] = o[s][0];
-          turn[ha * D + 16 * s + 8 + gid] = o[s][2];
+        if (wa) {
+          ta[16 * s] = o[s][0];
+          ta[16 * s + 8] = o[s][2];
         }
-        if (hb < nrep) {
-          turn[hb * D + 16 * s + gid] = o[s][1];
-          turn[hb * D + 16 * s + 8 + gid] = o[s][3];
+        if (wb) {
+          tb[16 * s] = o[s][1];
+          tb[16 * s + 8] = o[s][3];
         }
       }
       __syncwarp();
+      static_assert(3 * kTerm * 4 <= Cfg::kTileBytes, "the terms fit the K rows' place");
+      auto sums = [&](int e) {
+        float4 x = *reinterpret_cast<const float4*>(turn + e);
+        if constexpr (PAIR) {
+          const float4 y = *reinterpret_cast<const float4*>(turn + kTerm + e);
+          const float4 z = *reinterpret_cast<const float4*>(turn + 2 * kTerm + e);
+          x = make_float4(x.x + (y.x + z.x), x.y + (y.y + z.y), x.z + (y.z + z.z), x.w + (y.w + z.w));
+        }
+        return x;
+      };
       if (row_end && from_start) {
         uint16_t* dst = a.out + (static_cast<size_t>(cur.b) * a.Hq + cur.g * nrep) * D;
         for (int e = 4 * lane; e < (nrep * D + 127) / 128 * 128; e += 128) {   // the whole warp shuffles
           const int h = e / D;
           const float la = __shfl_sync(0xFFFFFFFFu, L0, h >> 1 & 3), lb = __shfl_sync(0xFFFFFFFFu, L1, h >> 1 & 3);
-          if (h < nrep) write_out(dst + e, h & 1 ? lb : la, *reinterpret_cast<const float4*>(turn + e));
+          if (h < nrep) write_out(dst + e, h & 1 ? lb : la, sums(e));
         }
       } else {
         // slot 0: the row began before this range; slot 1: it begins here and goes on
         const int cut = from_start ? 1 : 0;
         float* dst = my_part + cut * psize;
         for (int e = 4 * lane; e < nrep * D; e += 128)
-          *reinterpret_cast<float4*>(dst + e / D * PF + e % D) = *reinterpret_cast<const float4*>(turn + e);
+          *reinterpret_cast<float4*>(dst + e / D * PF + e % D) = sums(e);
         if (gid == 0 && ha < nrep) write_ml(dst + ha * PF + D, m0, L0);
         if (gid == 0 && hb < nrep) write_ml(dst + hb * PF + D, m1, L1);
         if (lane == 0) {
@@ -639,9 +688,10 @@ __global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(
 template <int D, int W>
 cudaError_t launch_dp(const DpArgs& a, int blocks, cudaStream_t s) {
   using Cfg = DpCfg<D, W>;
-  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(decode_paged_kernel<D, W>), Cfg::kSmemBytes);
+  auto* kernel = a.Hq <= 2 * a.c.Hkv ? decode_paged_kernel<D, W, true> : decode_paged_kernel<D, W, false>;
+  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), Cfg::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_after(decode_paged_kernel<D, W>, dim3(blocks), dim3(Cfg::kThreads), Cfg::kSmemBytes, s, a);
+  return launch_after(kernel, dim3(blocks), dim3(Cfg::kThreads), Cfg::kSmemBytes, s, a);
 }
 
 }  // namespace
@@ -668,9 +718,9 @@ cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, cons
   // d = 64: sixteen warps keep more scattered rows on their way (64 sequences with
   // lists of 2048 on 8 heads, selection included: 116 us, eight warps 139 us; 16 of 500
   // to 700 keys on 4 heads: 9.5 and 10.3 us); eight start and join sooner, which counts
-  // while there are few and short rows (one sequence of 301 keys, 4 heads: 7.6 and 7.0 us;
-  // of 2048: 9.6 and 8.9 us; of 4096: 10.2 and 10.0 us; of 32k: 16.9 and 17.4 us; of 512k: 94
-  // and 113 us; two of 301 keys: 7.7 and 7.1 us, of 131k: 54 and 62 us)
+  // while there are few and short rows (one sequence of 301 keys, 4 heads: 7.5 and 6.7 us;
+  // of 2048: 9.6 and 8.6 us; of 4096: 10.2 and 9.8 us; of 32k: 15.9 and 16.4 us; of 512k: 94
+  // and 115 us; two of 301 keys: 7.7 and 6.8 us, of 131k: 54 and 62 us)
   const bool few = lists.cap == 0 && 4 * c.B * c.Hkv <= nsm && c.longest <= kFewWarpsLength;
   return few ? launch_dp<64, 8>(a, blocks, s) : launch_dp<64, 16>(a, blocks, s);
 }
