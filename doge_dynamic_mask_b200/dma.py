@@ -450,6 +450,8 @@ def dma_decode_paged(q, k_pages, v_pages, dt_pages, page_table, lengths, keep_wi
                 ("page_table", page_table, i32, (B, max_pages), False), ("lengths", lengths, i32, (B,), False),
                 ("out", out, bf, (B, Hq, d), False),
                 ("workspace", workspace, workspace.dtype, workspace.shape, False))
+    if out.data_ptr() == q.data_ptr():
+        raise ValueError("out must not be q: blocks that share a row read q until the last one has joined it")
     _ok(_lib.dma_decode_paged(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), dt_pages.data_ptr(), page_table.data_ptr(),
         lengths.data_ptr(), B, max_pages, N, page_size, _page_stride(k_pages, v_pages), Hq, Hkv, d,

@@ -372,6 +372,7 @@ DMA_API dma_status_t dma_prologue_backward(const void* q, const void* k, int64_t
  *   workspace     >= 256 bytes, zeroed once (status word).  A token whose position lies outside
  *                 [0, max_pages * page_size) is reported as DMA_ERR_BAD_POSITION; its cache rows
  *                 are not written, its q_out and k_out rows are.  The same holds for a bad page.
+ * An infinite entry of v gives its token a dt of NaN (W_dt is multiplied in parts).
  * Two tokens must not share a cache row.  Outputs must not overlap inputs.
  *
  * dma_decode_paged: [DMA steps 3-4] for one new query per sequence, as
@@ -382,7 +383,7 @@ DMA_API dma_status_t dma_prologue_backward(const void* q, const void* k, int64_t
  *                 tokens that stay visible; pages in between may be gone).
  * Of those it keeps the keep_window_size best by dt (ties: lower index), and
  *   out[b, h, :] = sum_j p_j v_j,  p = softmax_fp32(scale * q_h . k_j + dt_j) over the kept keys.
- *   q, out        [B, Hq, d] bf16 (out written)
+ *   q, out        [B, Hq, d] bf16 (out written; it must not overlap q)
  *   lengths       [B] int32 in [0, max_pages * page_size]; 0 is an empty slot of a padded batch,
  *                 whose out row is zero.  Others are clamped and reported as DMA_ERR_BAD_LENGTH
  *   keep_window_size  any positive number, with fewer than 2^35 kept keys in all if every
@@ -390,7 +391,9 @@ DMA_API dma_status_t dma_prologue_backward(const void* q, const void* k, int64_t
  *                 dma_append_paged writes it
  *   workspace     dma_decode_paged_workspace_size(...) bytes, zeroed once (status word first)
  * Keys in a page outside the pool are not seen (and reported).  Rows of a page past the
- * sequence's length are never used and may hold anything.  The same call gives the same bits.
+ * sequence's length are never used and may hold anything.  An infinite entry of a
+ * kept v row gives its infinity or NaN (p is multiplied in three parts, of which some may
+ * be 0).  The same call gives the same bits.
  */
 DMA_API dma_status_t dma_append_paged(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
                                       int64_t v_stride, const float* q_norm_w, const float* k_norm_w, float eps,

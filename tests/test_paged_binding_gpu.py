@@ -70,3 +70,35 @@ def test_prologue_backward_without_a_workspace_zeroes_the_header_alone(dma):
     t = what_is_left(size, at)
     assert not t[:256].any()
     assert (t[256:] == 0xA5).float().mean() > 0.5
+
+
+def test_decode_refuses_to_write_its_query(dma):
+    """Blocks that share a row read q until the last one has joined it: in place would be a race."""
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda").to(torch.bfloat16)
+    q, kv, dt = rand(1, 4, 64), rand(4, 16, 2, 64), torch.rand((4, 2, 16), generator=gen, device="cuda")
+    table, lens = torch.arange(4, dtype=torch.int32, device="cuda")[None], torch.tensor([60], dtype=torch.int32, device="cuda")
+    before = q.clone()
+    with pytest.raises(ValueError, match="out must not be q"):
+        dma.dma_decode_paged(q, kv, kv, dt, table, lens, 2048, out=q)
+    assert torch.equal(q, before)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (8, 1, 128)])
+def test_infinite_values_show_where_they_are_kept_and_nowhere_else(dma, Hq, Hkv, d):
+    """A probability's three parts are not negative, so their products with an infinity are it, or NaN where a part is 0."""
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda").to(torch.bfloat16)
+    q, k, v, dt = rand(2, Hq, d), rand(8, 16, Hkv, d), rand(8, 16, Hkv, d), torch.rand((8, Hkv, 16), generator=gen, device="cuda")
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    lens = torch.tensor([60, 60], dtype=torch.int32, device="cuda")
+    want = dma.dma_decode_paged(q, k, v, dt, table, lens, 2048)
+    v[1, 3, 0, 7] = float("inf")                     # kept by sequence 0
+    v[7, 14, 0, 7] = float("inf")                    # past sequence 1's length
+    out = dma.dma_decode_paged(q, k, v, dt, table, lens, 2048)
+    rep = Hq // Hkv
+    got = out[0, :rep, 7]
+    assert (got.isnan() | (got == float("inf"))).all()
+    others = torch.ones_like(out, dtype=torch.bool)
+    others[0, :rep, 7] = False
+    assert torch.equal(out[others], want[others])
