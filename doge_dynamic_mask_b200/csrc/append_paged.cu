@@ -40,10 +40,13 @@
 // projection is 2 Hkv flops per byte of V: far below what tcgen05 is for, and a
 // 128-row tile would leave a decode step's few tokens on one SM.
 //
-// Measured.  32768 tokens, 16 + 8 heads of 128, K rows packed as well: 108 us for
-// 605 MB, 5.6 TB/s (94 us at the copy rate).  9 prompts of up to 2047 tokens, 8 + 4
-// heads of 64: 11.8 us for 43 MB, of which about 4 us are the start and W's split.
-// 57 single tokens: 5.6 us, a launch and four dependent memory latencies.
+// Measured.  32768 tokens, 16 + 8 heads of 128, K rows packed as well: 107 us for
+// 605 MB, 5.7 TB/s (94 us at the copy rate).  9 prompts of up to 2047 tokens, 8 + 4
+// heads of 64: 12.7 us for 43 MB, of which about 4 us are the start and W's split.
+// 57 single tokens: 5.5 us, a launch and four dependent memory latencies.  One to four
+// heads of each: 28 to 30 us for 21852 tokens of d = 128, whatever their number, against
+// 5 to 10 us at the copy rate: a warp step is four heads of one token, and fewer leave
+// its other rows empty.
 #include <algorithm>
 
 #include "rope.cuh"

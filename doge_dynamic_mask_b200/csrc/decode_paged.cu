@@ -29,10 +29,10 @@
 //
 // Measured.  Long rows kept whole (8 sequences of 64k to 128k keys, 8 heads of
 // 128) run at the copy rate: 480 us for 3.2 GB, 6.7 TB/s.  Kept lists of 2048 of
-// 32k to 64k keys, 64 sequences: about 97 us for 540 MB, 5.6 TB/s in scattered
+// 32k to 64k keys, 64 sequences: about 102 us for 540 MB, 5.3 TB/s in scattered
 // 256-byte rows.  Small calls are bound by the chain lengths, table, rows, pieces,
 // each a memory latency: 32 ragged sequences of up to 2048 keys of 4 heads of 64,
-// 14.3 us for 34 MB; one sequence of 301 keys, 6.5 us.
+// 14.8 us for 34 MB; one sequence of 301 keys, 6.6 us.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(
   const uint32_t U = total * static_cast<uint32_t>(c.Hkv);
   // few rows of like lengths: a block takes a row (its part of the axis begins at 0
   // then), and none joins with others.  48 sequences that see 1028 keys of 2 heads of
-  // 128 took 20.5 us over equal parts, 17.4 us so; one of 301 keys of 4 heads of 64,
-  // 9.0 and 7.5 us; at five tiles a warp instead of kRowSteps both are alike.
+  // 128 take 18.8 us over equal parts, 16.9 us so; one of 301 keys of 4 heads of 64,
+  // 7.2 and 6.6 us; at five tiles a warp instead of kRowSteps both are alike.
   most = __reduce_max_sync(0xFFFFFFFFu, most);
   const uint32_t rows = static_cast<uint32_t>(c.B) * static_cast<uint32_t>(c.Hkv);
   const bool by_row = rows <= gridDim.x && most * gridDim.x <= U + kRowSteps * kDpWarps * gridDim.x;
@@ -716,8 +716,8 @@ cudaError_t launch_attn_paged(const PagedCache& c, const PagedLists& lists, cons
   const int blocks = std::min(nsm, kPagedMaxBlocks);
   if (c.d == 128) return launch_dp<128, 8>(a, blocks, s);
   // d = 64: sixteen warps keep more scattered rows on their way (64 sequences with
-  // lists of 2048 on 8 heads, selection included: 116 us, eight warps 139 us; 16 of 500
-  // to 700 keys on 4 heads: 9.5 and 10.3 us); eight start and join sooner, which counts
+  // lists of 2048 on 8 heads, selection included: 121 us, eight warps 145 us; 16 of 500
+  // to 700 keys on 4 heads: 9.5 and 10.4 us); eight start and join sooner, which counts
   // while there are few and short rows (one sequence of 301 keys, 4 heads: 7.5 and 6.7 us;
   // of 2048: 9.6 and 8.6 us; of 4096: 10.2 and 9.8 us; of 32k: 15.9 and 16.4 us; of 512k: 94
   // and 115 us; two of 301 keys: 7.7 and 6.8 us, of 131k: 54 and 62 us)

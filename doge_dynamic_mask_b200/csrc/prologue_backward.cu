@@ -28,7 +28,9 @@
 //
 // Measured.  32768 tokens, 16 + 8 heads of 128: 115 us for 604 MB, 5.2 TB/s (94 us
 // at the copy rate).  16384 tokens, 8 + 4 heads of 64: 22 us for 75 MB, of which some
-// 6 us are the start and the join of the weight gradients (74 tokens take 5.6 us).
+// 6 us are the start and the join of the weight gradients (74 tokens take 5.6 us).  With
+// one to three heads of q and one or two of k, 21852 tokens of d = 128 take 31 us (5 to 10 us
+// at the copy rate): a warp step is four heads of one token, absent or not.
 // Half of the issue slots are used, by four warps a scheduler, which 128 registers a
 // thread allow; ten warps a block in 96 registers spilled: 165 us and 32 us.
 #include <algorithm>

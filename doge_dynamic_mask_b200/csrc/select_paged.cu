@@ -45,7 +45,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kSpSample = 512;           // sampled octs (runs of eight positions), at most
 constexpr int kSpSampleLong = 131072;    // rows up to this length take half of them (512 rows of 32k to 64k keys at w = 2048
-                                         // and 4000: 158 and 256 us; all of them 162 and 260; a quarter 157 and 289)
+                                         // and 4000, attention included: 162 and 260 us; all of them 166 and 264; a quarter 161 and 276)
 constexpr int kSpEdge = 512;             // keys inside the w-th key's bin
 constexpr int kSpMaxCluster = 8;         // CTAs of a row
 constexpr int kSpSpill = 128;            // keys of a CTA that found their thread's list full
@@ -169,8 +169,8 @@ __device__ __forceinline__ uint32_t load_oct(const PagedCache& c, const Row& r, 
 // A step of the collection: 32 octs from q0 on, eight keys of them per lane.  VEC:
 // an oct a lane; else lane l has every 32nd key from the l-th on, so that a load
 // of the warp reads neighbouring keys (64 sequences of 32k to 64k keys in pages of
-// five, the step with its attention: 480 us with an oct a lane, 277 us so; in pages
-// of 100, 208 and 223 us).
+// five, the step with its attention: 480 us with an oct a lane, 274 us so; in pages
+// of 100, 208 and 225 us).
 template <bool VEC>
 __device__ __forceinline__ int step_position(const Row& r, int q0, int e) {
   const int lane = threadIdx.x & 31;
@@ -756,10 +756,10 @@ cudaError_t launch_select_paged(const PagedCache& c, const PagedLists& lists, cu
   const int rows = c.B * c.Hkv;
   const bool vec = c.page_size % 8 == 0;
   // few rows: as many CTAs per row as the SMs hold at once, each with 4096 keys or
-  // more of the longest row (one sequence of 500k keys, 8 heads,
-  // attention included: 28.5 us on eight CTAs a row, 109 us on one; 4 rows of a window of
-  // 8196 keys on 4 heads in tables of 500k: 19.8 us on two CTAs a row, 33.2 us on the eight
-  // that the tables' length would ask for)
+  // more of the longest row (one sequence of 500k keys, 8 heads, attention included:
+  // 28.5 us on eight CTAs a row, 109 us on one; 4 sequences with a window of 8192 keys, 4
+  // heads, in tables of 500k: 20 us on two CTAs a row, 33 us on the eight that the tables'
+  // length would ask for)
   int csize = 1;
   while (csize < kSpMaxCluster && 2LL * csize * rows <= nsm && c.longest >= 4096 * 2 * csize) csize *= 2;
   if (csize > 1)
@@ -767,7 +767,7 @@ cudaError_t launch_select_paged(const PagedCache& c, const PagedLists& lists, cu
                : launch_sp<1024, false, true>(c, lists, rows, csize, s);
   // many rows: one CTA each, or as many as give the lists of a large window room
   // while two CTAs share an SM (512 rows of 32k to 64k keys at w = 4000, the step with
-  // its attention: 306 us with one CTA an SM, 258 us so)
+  // its attention: 306 us with one CTA an SM, 260 us so)
   for (; csize < kSpMaxCluster; csize *= 2) {
     const Share share = share_of(c, 512 * csize);
     if (share.mean + 2.0 * share.deviation <= most_room<512>(2)) break;
