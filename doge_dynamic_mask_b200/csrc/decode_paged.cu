@@ -508,9 +508,9 @@ __global__ void __launch_bounds__(DpCfg<D, W>::kThreads, 1) decode_paged_kernel(
     };
     if constexpr (PAIR) {
       auto mine = [&](float p, float r, float u) { return t4 == 0 ? p : t4 == 1 ? r : t4 == 2 ? u : 0.0f; };
-      const uint32_t m0 = transpose8x8(pack_leading(mine(p00, r00, u00), mine(p01, r01, u01)));
-      const uint32_t m1 = transpose8x8(pack_leading(mine(p10, r10, u10), mine(p11, r11, u11)));
-      values([&](auto& t, const auto& va) { term(t, va, m0, m1); });
+      const uint32_t pm0 = transpose8x8(pack_leading(mine(p00, r00, u00), mine(p01, r01, u01)));
+      const uint32_t pm1 = transpose8x8(pack_leading(mine(p10, r10, u10), mine(p11, r11, u11)));
+      values([&](auto& t, const auto& va) { term(t, va, pm0, pm1); });
     } else {
       const uint32_t ph0 = transpose8x8(pack_leading(p00, p01)), ph1 = transpose8x8(pack_leading(p10, p11));
       const uint32_t pe0 = transpose8x8(pack_leading(r00, r01)), pe1 = transpose8x8(pack_leading(r10, r11));
